@@ -119,6 +119,69 @@ MOE_API int moe_route(const moe_shape* shape, const void* u, int32_t u_dtype, co
               const float* bias, int32_t* top_idx, float* top_w, float* probs, float* logits,
               void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------------------------------- scored routing */
+/* Routing by scores, from the router logits z [T][N] fp32:
+ *   s_j = sigmoid(z_j) (MOE_SCORE_SIGMOID), or softmax(z)_j (MOE_SCORE_SOFTMAX)
+ *   c_j = s_j + b_j     b: a bias that balances the loads; it takes part in
+ *                       the selection and not in the weights
+ *   groups: experts g N/n_group .. (g+1) N/n_group - 1 form group g, whose
+ *     score is the sum of its group_top (1 or 2) largest c; a token uses the
+ *     top_group best groups (ties to the lower group)
+ *   S = the k largest c of the experts of those groups, largest first, ties
+ *     to the lower expert
+ *   a_i = scale s_i / sum_{j in S} s_j  (shape->renorm = 1)  or  scale s_i
+ * s is computed in double and rounded to fp32 once, and c and the groups'
+ * scores are one fp32 addition each, so the selection can be reproduced.
+ * A logit of -infinity scores 0; a NaN logit scores NaN (under softmax a NaN
+ * or +infinity makes the row's scores NaN).  A NaN c ranks below every value;
+ * the k experts are distinct whatever the logits hold.  When every selected
+ * score is 0 the renormalised weights are 0. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+typedef struct {
+  int32_t score;     /* MOE_SCORE_* */
+  int32_t n_group;   /* 1..32, a divisor of N; 1: no groups */
+  int32_t top_group; /* 1..n_group, top_group N / n_group >= k */
+  int32_t group_top; /* 1 or 2, at most N / n_group */
+  float scale;       /* factor of the combine weights */
+} moe_gating;
+
+/* The selection from logits that the caller holds.  shape: T, N, k and renorm
+ * are used (1 <= N <= 1024, 1 <= k <= min(N, 32)).
+ *   logits [T][N] fp32;  bias [N] fp32 or NULL
+ *   top_idx [T][k] int32 out, top_w [T][k] fp32 out: a
+ *   scores [T][N] fp32 out or NULL: s (may be logits itself)
+ * logits and scores 16-byte aligned.  MOE_ERR_INVALID_ARG for a size outside
+ * the limits or a NULL or misaligned pointer; T = 0 is a no-op. */
+MOE_API int moe_route_select(const moe_shape* shape, const moe_gating* gating,
+                             const float* logits, const float* bias, int32_t* top_idx,
+                             float* top_w, float* scores, void* stream);
+
+/* moe_route_select after the logits of moe_route (W_route u in its fixed fp32
+ * order, no bias on them): u [T][d] in u_dtype, w_route [N][d] fp32, bias the
+ * selection's.  logits [T][N] fp32 out or NULL (then they stay in ws, of
+ * moe_route_scored_workspace_bytes(shape)). */
+MOE_API size_t moe_route_scored_workspace_bytes(const moe_shape* shape);
+MOE_API int moe_route_scored(const moe_shape* shape, const moe_gating* gating, const void* u,
+                             int32_t u_dtype, const float* w_route, const float* bias,
+                             int32_t* top_idx, float* top_w, float* scores, float* logits,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient to the logits with the selection held fixed (it is piecewise
+ * constant; the bias gets none):
+ *   dz [T][N] fp32 out = dL/dz of  sum d_top_w . top_w + sum d_scores . s
+ * from the forward's logits and top_idx, d_top_w [T][k] fp32 and d_scores
+ * [T][N] fp32 or NULL (e.g. a balance loss's).  dz may be d_scores itself.
+ * An expert that stands twice in a row of top_idx counts twice; an index
+ * outside [0, N) records MOE_ERR_BOUNDS in the device status word and its slot
+ * counts as absent.  Where the selected scores' sum is 0, renormalised
+ * weights give no gradient.  Errors as moe_route_select. */
+MOE_API int moe_route_select_bwd(const moe_shape* shape, const moe_gating* gating,
+                                 const float* logits, const int32_t* top_idx,
+                                 const float* d_top_w, const float* d_scores, float* dz,
+                                 void* stream);
+
 /* ------------------------------------------------------------- aux stats */
 /* Switch balancing statistics (tutorial §3.4) from probs [T][N] and top_idx:
  *   f[i] = fraction of tokens whose argmax (slot 0) is i
@@ -413,6 +476,118 @@ MOE_API int moe_latent_bwd(const moe_shape* shape, const moe_layer_weights* w,
                            const moe_latent_weights* lw, const void* x, const void* dy,
                            const moe_layer_outputs* fwd, const moe_latent_grads* grads, void* ws,
                            size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------ block norms */
+/* The norms around a block of the residual stream x, with the block's output
+ * y, its gate and the residual scale, in one pass:
+ *   n  = y / sqrt(mean(y^2) + eps) * w_post       (w_post NULL: n = y)
+ *   x' = res_scale x + out_scale gate n           x_out, in the storage type
+ *   u  = x' / sqrt(mean(x'^2) + eps) * w_pre      of x' as stored (w_pre NULL:
+ *                                                 not formed)
+ * y NULL: no block's output is added, x' is x (res_scale unused) and u is
+ * its norm; w_post and gate are then NULL and x_out is not written.
+ *   x, y, x_out, u [T][d] in dtype (MOE_F32, MOE_BF16 or MOE_F16)
+ *   w_post, w_pre [d] fp32
+ *   gate: MOE_GATE_NONE NULL; MOE_GATE_CHANNEL [d] fp32; MOE_GATE_TOKEN [T]
+ *     fp32; MOE_GATE_FULL [T][d] in dtype
+ * d a multiple of 8, at most 16384; eps > 0.  Row sums are fp32.  x_out may
+ * be x.  All pointers but a token gate 16-byte aligned.  T = 0 is a no-op.
+ * MOE_ERR_INVALID_ARG for a size, a kind or a combination outside these. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN 2
+#define MOE_GATE_FULL 3
+
+typedef struct {
+  int32_t T;
+  int32_t d;
+  int32_t gate; /* MOE_GATE_* */
+  float res_scale;
+  float out_scale;
+  float eps;
+} moe_block_norm;
+
+MOE_API int moe_block_norm_fwd(const moe_block_norm* norm, int32_t dtype, const void* x,
+                               const void* y, const float* w_post, const void* gate,
+                               const float* w_pre, void* x_out, void* u, void* stream);
+
+/* Gradients of L = sum dx_out . x' + sum du . u, with u a function of x' as
+ * stored:
+ *   dx [T][d]     dL/dx, in grad_dtype (MOE_F32 or dtype); may be dx_out
+ *   dy [T][d]     dL/dy, in dtype (what moe_layer_bwd takes); NULL: the forward
+ *                 had no y
+ *   dgate         as gate: [d] fp32, [T] fp32 or [T][d] in dtype
+ *   dw_post, dw_pre [d] fp32
+ * dgate, dw_post and dw_pre are NULL exactly where gate, w_post and w_pre are.
+ * All outputs are fully overwritten; sums over the tokens are fp32 in a fixed
+ * order. */
+typedef struct {
+  void* dx;
+  void* dy;
+  void* dgate;
+  float* dw_post;
+  float* dw_pre;
+} moe_block_norm_grads;
+
+/* x_out (read where w_pre is set; x itself where the forward had no y) and y
+ * (read where w_post or gate is set) in dtype; dx_out [T][d] in grad_dtype, or
+ * NULL for zero where w_pre is set; du [T][d] in grad_dtype, with w_pre.
+ * Row norms are formed again from x_out and y.  T = 0 zeroes dw_post, dw_pre
+ * and a channel gate's dgate.  MOE_ERR_UNSUPPORTED for another grad_dtype. */
+MOE_API size_t moe_block_norm_bwd_workspace_bytes(const moe_block_norm* norm);
+MOE_API int moe_block_norm_bwd(const moe_block_norm* norm, int32_t dtype, int32_t grad_dtype,
+                               const void* x_out, const void* y, const float* w_post,
+                               const void* gate, const float* w_pre, const void* dx_out,
+                               const void* du, const moe_block_norm_grads* grads, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------- 8-bit integer products */
+/* Values as codes -127..127 with one fp32 scale per row: s = amax(row) / 127
+ * (1 for a zero row), code = x / s rounded to nearest even, each division one
+ * fp32 operation.  A row with an infinity or a NaN has that scale, so that
+ * its products are NaN.  x [rows][cols] in x_dtype (MOE_F32, MOE_BF16 or
+ * MOE_F16), cols a multiple of 16, codes [rows][cols], scales [rows].  Errors
+ * as moe_quantize_e4m3_rows. */
+MOE_API int moe_quantize_i8_rows(int64_t rows, int32_t cols, const void* x, int32_t x_dtype,
+                                 int8_t* codes, float* scales, void* stream);
+
+/* Grouped product of codes: for every row r of group e (offsets[e] <= r <
+ * offsets[e+1]):
+ *   y[r][j] = x_scale[r] w_scale[e][j] sum_c x[r][c] w[e][j][c]
+ * x [rows][K] codes with a scale per row (token), w [G][n][K] codes with a
+ * scale per output channel [G][n], y [rows][n] in y_dtype (MOE_F32, MOE_BF16
+ * or MOE_F16).  The sum is exact in s32 (codes may be -128), then one fp32
+ * product by each scale and one rounding to y_dtype.  offsets [G+1] device,
+ * or NULL with G = 1: all rows.  Rows outside every group are left as they
+ * were; a range outside [0, rows] records MOE_ERR_BOUNDS in the device status
+ * word and its group is skipped.  K a multiple of 16 up to 131056, any n >= 1,
+ * 1 <= G <= 1024.  x, w and y 16-byte aligned.
+ * ws: moe_grouped_gemm_i8_workspace_bytes (may be 0 -> ws NULL). */
+MOE_API size_t moe_grouped_gemm_i8_workspace_bytes(int32_t rows, int32_t G, int32_t K, int32_t n);
+MOE_API int moe_grouped_gemm_i8(int32_t rows, int32_t G, int32_t K, int32_t n, const int8_t* x,
+                                const float* x_scale, const int32_t* offsets, const int8_t* w,
+                                const float* w_scale, void* y, int32_t y_dtype, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* The grouped expert FFN of moe_expert_ffn with 8-bit integer operands:
+ * x_rows [T*k][width] codes with x_scale [T*k], the experts' codes (gate, up
+ * [N][h][width], down [N][width][h]) with their row scales, SwiGLU or SiTU-GLU;
+ * H is rounded to bf16, then quantised per row for the down product; y_rows
+ * [T*k][width] fp32, F(u) of each grouped row (not weighted).  width and h
+ * multiples of 128.  ws: moe_expert_ffn_i8_workspace_bytes.  Errors as
+ * moe_expert_ffn. */
+typedef struct {
+  const float* gate_scale; /* [N * h] row scales of w_gate's codes */
+  const float* up_scale;   /* [N * h] row scales of w_up's codes */
+  const float* down_scale; /* [N * width] row scales of w_down's codes */
+} moe_i8_scales;
+
+MOE_API size_t moe_expert_ffn_i8_workspace_bytes(const moe_shape* shape);
+MOE_API int moe_expert_ffn_i8(const moe_shape* shape, int32_t width, const int8_t* x_rows,
+                              const float* x_scale, const int32_t* offsets, const int8_t* w_gate,
+                              const int8_t* w_up, const int8_t* w_down,
+                              const moe_i8_scales* scales, const moe_act* act, float* y_rows,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------- q4_0 decode */
 /* Small-batch decode with q4_0 experts (deployment notes "Kestrel-MCU notes

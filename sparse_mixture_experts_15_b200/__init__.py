@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 F32, BF16, F16, Q4_0, E4M3 = 0, 1, 2, 3, 4
 ACT_SWIGLU, ACT_SITU_GLU = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -69,6 +71,24 @@ class MoeE4M3Scales(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("gate_scale", "up_scale", "down_scale")]
 
 
+class MoeGating(ctypes.Structure):
+    _fields_ = [("score", _i32), ("n_group", _i32), ("top_group", _i32), ("group_top", _i32),
+                ("scale", _f32)]
+
+
+class MoeBlockNorm(ctypes.Structure):
+    _fields_ = [("T", _i32), ("d", _i32), ("gate", _i32), ("res_scale", _f32),
+                ("out_scale", _f32), ("eps", _f32)]
+
+
+class MoeBlockNormGrads(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("dx", "dy", "dgate", "dw_post", "dw_pre")]
+
+
+class MoeI8Scales(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("gate_scale", "up_scale", "down_scale")]
+
+
 class MoeEpBuffers(ctypes.Structure):
     _fields_ = [("world", _i32), ("rank", _i32), ("recv_capacity", _i32)] + [
         (n, _vp) for n in ("recv_rows", "recv_w", "out_rows", "arrive", "done", "peer_recv_rows",
@@ -76,10 +96,29 @@ class MoeEpBuffers(ctypes.Structure):
 
 
 _P_SHAPE = ctypes.POINTER(MoeShape)
+_P_GATING = ctypes.POINTER(MoeGating)
+_P_NORM = ctypes.POINTER(MoeBlockNorm)
 _PROTOS = {
     "moe_capacity": (_i32, [_i64, _i32, _i32, _f64, ctypes.POINTER(_i32)]),
     "moe_route_workspace_bytes": (_sz, [_P_SHAPE]),
     "moe_route": (_i32, [_P_SHAPE, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_select": (_i32, [_P_SHAPE, _P_GATING] + [_vp] * 6),
+    "moe_route_scored_workspace_bytes": (_sz, [_P_SHAPE]),
+    "moe_route_scored": (_i32, [_P_SHAPE, _P_GATING, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _sz, _vp]),
+    "moe_route_select_bwd": (_i32, [_P_SHAPE, _P_GATING] + [_vp] * 6),
+    "moe_block_norm_fwd": (_i32, [_P_NORM, _i32] + [_vp] * 8),
+    "moe_block_norm_bwd_workspace_bytes": (_sz, [_P_NORM]),
+    "moe_block_norm_bwd": (_i32, [_P_NORM, _i32, _i32] + [_vp] * 7 +
+                           [ctypes.POINTER(MoeBlockNormGrads), _vp, _sz, _vp]),
+    "moe_quantize_i8_rows": (_i32, [_i64, _i32, _vp, _i32, _vp, _vp, _vp]),
+    "moe_grouped_gemm_i8_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_grouped_gemm_i8": (_i32, [_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                   _vp, _sz, _vp]),
+    "moe_expert_ffn_i8_workspace_bytes": (_sz, [_P_SHAPE]),
+    "moe_expert_ffn_i8": (_i32, [_P_SHAPE, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 ctypes.POINTER(MoeI8Scales), ctypes.POINTER(MoeAct), _vp, _vp,
+                                 _sz, _vp]),
     "moe_aux_stats_workspace_bytes": (_sz, [_i32]),
     "moe_aux_stats": (_i32, [_i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_permute_workspace_bytes": (_sz, [_P_SHAPE]),
@@ -235,6 +274,14 @@ def shape(T, d, N, k, h=0, renorm=1, capacity=0) -> MoeShape:
 
 def act(kind=ACT_SWIGLU, beta_gate=0.0, beta_up=0.0) -> MoeAct:
     return MoeAct(kind, beta_gate, beta_up)
+
+
+def gating(score=SCORE_SOFTMAX, n_group=1, top_group=1, group_top=1, scale=1.0) -> MoeGating:
+    return MoeGating(score, n_group, top_group, group_top, scale)
+
+
+def block_norm(T, d, gate=GATE_NONE, res_scale=1.0, out_scale=1.0, eps=1e-6) -> MoeBlockNorm:
+    return MoeBlockNorm(T, d, gate, res_scale, out_scale, eps)
 
 
 # ------------------------------------------------------------- entry points
@@ -515,6 +562,200 @@ def moe_latent_fwd_e4m3(s: MoeShape, w_route, w_gate, w_up, w_down, gate_scale, 
     _check(_lib.moe_latent_fwd_e4m3(ctypes.byref(s), ctypes.byref(W), ctypes.byref(sc),
                                     ctypes.byref(lw), _ptr(x), _ptr(y), ctypes.byref(O),
                                     _ptr(wbuf), wlen, _stream(stream)), "moe_latent_fwd_e4m3")
+
+# -------------------------------- scored routing, block norms, 8-bit integers
+# These calls run on the device of their tensors, which must be one device:
+# its current stream unless one is given, whatever device is current.
+class _Call:
+    """One call's tensors: take() checks one as _need and _ptr do, and that it
+    is on the call's device (that of the first), and returns its address."""
+
+    def __init__(self):
+        import torch
+        self.torch, self.device = torch, None
+
+    def take(self, what, t, n, dtypes):
+        if t is None:
+            return None
+        if t.numel() < n:
+            raise ValueError(f"{what}: {t.numel()} elements, the call needs at least {n}")
+        if t.dtype not in dtypes:
+            names = " or ".join(str(x).replace("torch.", "") for x in dtypes)
+            raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, "
+                             f"the call needs {names}")
+        p = _ptr(t)
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{what}: on {t.device}, the call's other tensors on {self.device}")
+        return p
+
+    def workspace(self, nbytes, ws):
+        """(address, bytes) of a workspace of the call's device; the tensor is
+        kept until the call has been made."""
+        if nbytes == 0:
+            return None, 0
+        self.ws, n = _ws(nbytes, self.device, ws)
+        if self.ws.device != self.device:
+            raise ValueError(f"ws: on {self.ws.device}, the call's tensors on {self.device}")
+        return _ptr(self.ws), n
+
+    def run(self, where, stream, *args):
+        if self.device is None:
+            raise ValueError(f"{where}: no tensor to take the device from")
+        cuda, fn = self.torch.cuda, getattr(_lib, where)
+        if stream is None:
+            stream = cuda.current_stream(self.device).cuda_stream
+        if cuda.current_device() == self.device.index:
+            _check(fn(*args, int(stream)), where)
+        else:
+            with cuda.device(self.device):
+                _check(fn(*args, int(stream)), where)
+
+
+def moe_route_select(s: MoeShape, g: MoeGating, logits, top_idx, top_w, bias=None, scores=None,
+                     stream=None):
+    """Selection and weights from the router logits (include/moe.h)."""
+    c = _Call()
+    f32, i32 = (c.torch.float32,), (c.torch.int32,)
+    TN, Tk = s.T * s.N, s.T * s.k
+    c.run("moe_route_select", stream, ctypes.byref(s), ctypes.byref(g),
+          c.take("logits", logits, TN, f32), c.take("bias", bias, s.N, f32),
+          c.take("top_idx", top_idx, Tk, i32), c.take("top_w", top_w, Tk, f32),
+          c.take("scores", scores, TN, f32))
+
+
+def moe_route_scored(s: MoeShape, g: MoeGating, u, w_route, top_idx, top_w, bias=None,
+                     scores=None, logits=None, ws=None, stream=None):
+    """Router logits and the selection from them; bias is the selection's."""
+    c = _Call()
+    t = c.torch
+    f32, i32 = (t.float32,), (t.int32,)
+    TN, Tk = s.T * s.N, s.T * s.k
+    args = (c.take("u", u, s.T * s.d, (t.float32, t.bfloat16, t.float16)), _dtype_code(u),
+            c.take("w_route", w_route, s.N * s.d, f32), c.take("bias", bias, s.N, f32),
+            c.take("top_idx", top_idx, Tk, i32), c.take("top_w", top_w, Tk, f32),
+            c.take("scores", scores, TN, f32), c.take("logits", logits, TN, f32))
+    nb = 0 if logits is not None else _lib.moe_route_scored_workspace_bytes(ctypes.byref(s))
+    c.run("moe_route_scored", stream, ctypes.byref(s), ctypes.byref(g), *args,
+          *c.workspace(nb, ws))
+
+
+def moe_route_select_bwd(s: MoeShape, g: MoeGating, logits, top_idx, d_top_w, dz, d_scores=None,
+                         stream=None):
+    """Gradient of the weights (and scores) to the router logits."""
+    c = _Call()
+    f32 = (c.torch.float32,)
+    TN, Tk = s.T * s.N, s.T * s.k
+    c.run("moe_route_select_bwd", stream, ctypes.byref(s), ctypes.byref(g),
+          c.take("logits", logits, TN, f32), c.take("top_idx", top_idx, Tk, (c.torch.int32,)),
+          c.take("d_top_w", d_top_w, Tk, f32), c.take("d_scores", d_scores, TN, f32),
+          c.take("dz", dz, TN, f32))
+
+
+def _gate_args(b: MoeBlockNorm, c: _Call, what, t, dt):
+    n, types = {GATE_CHANNEL: (b.d, (c.torch.float32,)), GATE_TOKEN: (b.T, (c.torch.float32,)),
+                GATE_FULL: (b.T * b.d, dt)}.get(b.gate, (0, dt))
+    return c.take(what, t, n, types)
+
+
+def moe_block_norm_fwd(b: MoeBlockNorm, x, y=None, w_post=None, gate=None, w_pre=None, x_out=None,
+                       u=None, stream=None):
+    """x_out = res_scale x + out_scale gate norm(y) and u = norm(x_out)."""
+    c = _Call()
+    t = c.torch
+    n, f32 = b.T * b.d, (t.float32,)
+    px = c.take("x", x, n, (t.float32, t.bfloat16, t.float16))
+    dt = (x.dtype,)
+    c.run("moe_block_norm_fwd", stream, ctypes.byref(b), _dtype_code(x), px,
+          c.take("y", y, n, dt), c.take("w_post", w_post, b.d, f32),
+          _gate_args(b, c, "gate", gate, dt), c.take("w_pre", w_pre, b.d, f32),
+          c.take("x_out", x_out, n, dt), c.take("u", u, n, dt))
+
+
+def moe_block_norm_bwd_workspace_bytes(b: MoeBlockNorm) -> int:
+    return int(_lib.moe_block_norm_bwd_workspace_bytes(ctypes.byref(b)))
+
+
+def moe_block_norm_bwd(b: MoeBlockNorm, dx_out, grads: dict, x_out=None, y=None, w_post=None,
+                       gate=None, w_pre=None, du=None, ws=None, stream=None):
+    """Gradients of moe_block_norm_fwd: grads holds the outputs dx, dy (None
+    or absent: the forward had no y), dgate, dw_post and dw_pre.  The storage
+    type is that of x_out, y or dy, the gradients' type that of dx."""
+    c = _Call()
+    t = c.torch
+    n, f32, act = b.T * b.d, (t.float32,), (t.float32, t.bfloat16, t.float16)
+    dx = grads["dx"]
+    like = next((v for v in (x_out, y, grads.get("dy")) if v is not None), dx)
+    px = c.take("dx", dx, n, act)
+    gt, dt = (dx.dtype,), (like.dtype,)
+    G = MoeBlockNormGrads(px, c.take("dy", grads.get("dy"), n, dt),
+                          _gate_args(b, c, "dgate", grads.get("dgate"), dt),
+                          c.take("dw_post", grads.get("dw_post"), b.d, f32),
+                          c.take("dw_pre", grads.get("dw_pre"), b.d, f32))
+    args = (c.take("x_out", x_out, n, dt), c.take("y", y, n, dt),
+            c.take("w_post", w_post, b.d, f32), _gate_args(b, c, "gate", gate, dt),
+            c.take("w_pre", w_pre, b.d, f32), c.take("dx_out", dx_out, n, gt),
+            c.take("du", du, n, gt))
+    c.run("moe_block_norm_bwd", stream, ctypes.byref(b), _dtype_code(like), _dtype_code(dx), *args,
+          ctypes.byref(G), *c.workspace(moe_block_norm_bwd_workspace_bytes(b), ws))
+
+
+def moe_quantize_i8_rows(x, codes, scales, stream=None):
+    """8-bit integer codes and per-row fp32 scales of x [rows][cols]."""
+    c = _Call()
+    t = c.torch
+    rows, cols = x.shape
+    c.run("moe_quantize_i8_rows", stream, rows, cols,
+          c.take("x", x, rows * cols, (t.float32, t.bfloat16, t.float16)), _dtype_code(x),
+          c.take("codes", codes, rows * cols, (t.int8,)),
+          c.take("scales", scales, rows, (t.float32,)))
+
+
+def moe_grouped_gemm_i8_workspace_bytes(rows: int, G: int, K: int, n: int) -> int:
+    return int(_lib.moe_grouped_gemm_i8_workspace_bytes(rows, G, K, n))
+
+
+def moe_grouped_gemm_i8(x, x_scale, w, w_scale, y, offsets=None, ws=None, stream=None):
+    """y[r] = x_scale[r] w_scale[e] * (w[e] x[r]) for the rows r of group e:
+    x [rows][K] and w [G][n][K] (or [n][K]) codes, y [rows][n]."""
+    c = _Call()
+    t = c.torch
+    (rows, K), n, G = x.shape, w.shape[-2], w.shape[0] if w.dim() == 3 else 1
+    if w.shape[-1] != K:
+        raise ValueError(f"w: rows of {w.shape[-1]} codes, x has rows of {K}")
+    args = (c.take("x", x, rows * K, (t.int8,)), c.take("x_scale", x_scale, rows, (t.float32,)),
+            c.take("offsets", offsets, G + 1, (t.int32,)), c.take("w", w, G * n * K, (t.int8,)),
+            c.take("w_scale", w_scale, G * n, (t.float32,)),
+            c.take("y", y, rows * n, (t.float32, t.bfloat16, t.float16)), _dtype_code(y))
+    nb = _lib.moe_grouped_gemm_i8_workspace_bytes(rows, G, K, n)
+    c.run("moe_grouped_gemm_i8", stream, rows, G, K, n, *args, *c.workspace(nb, ws))
+
+
+def moe_expert_ffn_i8_workspace_bytes(s: MoeShape) -> int:
+    return int(_lib.moe_expert_ffn_i8_workspace_bytes(ctypes.byref(s)))
+
+
+def moe_expert_ffn_i8(s: MoeShape, width: int, x_rows, x_scale, offsets, w_gate, w_up, w_down,
+                      gate_scale, up_scale, down_scale, y_rows, a: MoeAct | None = None, ws=None,
+                      stream=None):
+    """Grouped expert FFN with 8-bit integer operands (include/moe.h); codes
+    are int8 tensors, scales fp32, y_rows fp32 [T*k][width]."""
+    a = a or act()
+    c = _Call()
+    t = c.torch
+    rows, f32, i8 = s.T * s.k, (t.float32,), (t.int8,)
+    args = (c.take("x_rows", x_rows, rows * width, i8), c.take("x_scale", x_scale, rows, f32),
+            c.take("offsets", offsets, s.N + 1, (t.int32,)),
+            c.take("w_gate", w_gate, s.N * s.h * width, i8),
+            c.take("w_up", w_up, s.N * s.h * width, i8),
+            c.take("w_down", w_down, s.N * width * s.h, i8))
+    S = MoeI8Scales(c.take("gate_scale", gate_scale, s.N * s.h, f32),
+                    c.take("up_scale", up_scale, s.N * s.h, f32),
+                    c.take("down_scale", down_scale, s.N * width, f32))
+    y = c.take("y_rows", y_rows, rows * width, f32)
+    c.run("moe_expert_ffn_i8", stream, ctypes.byref(s), width, *args, ctypes.byref(S),
+          ctypes.byref(a), y, *c.workspace(moe_expert_ffn_i8_workspace_bytes(s), ws))
 
 
 def q4_layer(w_route, gate_qs, gate_scales, up_qs, up_scales, down_qs, down_scales,

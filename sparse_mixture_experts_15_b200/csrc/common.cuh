@@ -273,6 +273,9 @@ int launch_route(const moe_shape& s, const void* u, int32_t u_dtype, const float
                  const float* bias, int32_t* top_idx, float* top_w, float* probs, float* logits,
                  void* ws, cudaStream_t st, int32_t* hist = nullptr);
 int route_tokens_per_block(int N);
+// z [T][N] = the router logits (+ bias, nullable) in moe_route's order.
+int launch_route_logits(const moe_shape& s, const void* u, int32_t u_dtype, const float* w_route,
+                        const float* bias, float* z, cudaStream_t st);
 // Permutation in one launch from the router's per-block counts (few experts;
 // dispatch_small_ok says when): see dispatch_small in permute.cu.
 bool dispatch_small_ok(const moe_shape& s);
@@ -335,7 +338,10 @@ int launch_ffn_fused(int G, int64_t R, int width, int h, const __nv_bfloat16* x_
                      void* y_rows, cudaStream_t st, const float* row_w = nullptr);
 
 // Grouped tcgen05 GEMM helpers (gemm_tc.cu).
-enum TcMode { MODE_GATEUP = 0, MODE_STORE_F32 = 1, MODE_STORE_BF16 = 2 };
+// (MODE_STORE_F16: 8-bit integer operands only)
+enum TcMode { MODE_GATEUP = 0, MODE_STORE_F32 = 1, MODE_STORE_BF16 = 2, MODE_STORE_F16 = 3 };
+// Operand types of a grouped GEMM.
+enum TcOps { OPS_BF16 = 0, OPS_E4M3 = 1, OPS_I8 = 2 };
 
 // One K-segment of a store-mode GEMM: A rows (weights) and B rows (tokens).
 struct TcSeg {
@@ -349,24 +355,29 @@ struct TcSeg {
   int bcol;           // column offset into B
 };
 
-// E4M3 operands of a grouped GEMM: codes in the operand arrays, fp32 scales
-// per row of A (gate/up: gate rows, up rows) and per row of B (nullable: 1).
+// E4M3 or 8-bit integer operands of a grouped GEMM: codes in the operand
+// arrays, fp32 scales per row of A (gate/up: gate rows, up rows) and per row
+// of B (nullable: 1).
 struct TcF8 {
   const float* a_scale[2];
   const float* b_scale;
+  int kind = OPS_E4M3;
 };
 
 // Gate/up GEMM with the fused activation: for group g and its rows of X,
 // out[row][g * out_col_group + j] = act(X W_gate[g]^T, X W_up[g]^T)[j] as bf16
 // (f8 == nullptr: bf16 X and weights), or as E4M3 codes with no scale (f8:
-// E4M3 X and weights with their row scales; K a multiple of 128).
+// E4M3 X and weights with their row scales; K a multiple of 128), or as bf16
+// (f8 with kind OPS_I8).
 // offsets == nullptr: every group uses rows [0, T) of X.
 int tc_gateup(const int32_t* offsets, int T, int G, const void* X, int64_t x_rows, int K,
               const void* w_gate, const void* w_up, int hidden, const moe_act& act, void* out,
               int out_ld, int out_col_group, cudaStream_t st, const TcF8* f8 = nullptr);
 // Store-mode GEMM over 1..3 K-segments accumulated into one fp32 tile:
 // out[row][g * m_rows + m] = sum_s A_s[g * a_rows + arow_s + m] . B_s[row][bcol_s ...].
-// f8: one segment of E4M3 operands, fp32 output scaled by the row scales.
+// f8: one segment of E4M3 operands, fp32 output scaled by the row scales; or
+// of 8-bit integers, with any m_rows, K a multiple of 16 and fp32, bf16 or fp16
+// output.
 // b_row_scale (nullable): a factor per token row, applied to the fp32 result
 // before the store (the combine weights of the grouped rows); with f8, its
 // b_scale plays this part.

@@ -1,0 +1,486 @@
+// Scored routing: softmax or sigmoid scores of the router's logits, a bias
+// that takes part in the selection only, expert groups, top-k and the combine
+// weights, and the gradient of the weights and scores to the logits.
+//
+//   s_j = sigmoid(z_j)  or  exp(z_j - max z) / sum exp(z - max z), to fp32
+//   c_j = s_j + b_j                                            (fp32)
+//   a group's score = the sum of its group_top largest c; the top_group best
+//   groups are kept (ties to the lower group); top_idx = the k largest c
+//   of their experts, ties to the lower expert
+//   a_i = scale s_i / sum_{selected} s   or   scale s_i
+//
+// The selection is a decision on the values s_j + b_j, and a score that is off
+// by one rounding can turn it.  So s is formed in double, to a relative error
+// below 2^-41, and rounded to fp32 once: it is the correctly rounded score but
+// for about one in 10^5, which then is off by one rounding.
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSelWarps = 4;  // tokens of a CTA, one warp each
+
+// 1 / x for x >= 1: the approximate instruction and two Newton steps.
+__device__ __forceinline__ double recip(double x) {
+  double r;
+  asm("rcp.approx.ftz.f64 %0, %1;" : "=d"(r) : "d"(x));
+  r = fma(r, fma(-x, r, 1.0), r);
+  return fma(r, fma(-x, r, 1.0), r);
+}
+
+// exp(x) for |x| <= 150: x = n ln 2 + r with |r| <= ln 2 / 2, the Taylor sum of
+// exp(r) to r^10 / 10! (the rest is below 2^-42), times 2^n in the exponent.
+// n is rounded by adding 1.5 2^52, which leaves it in the low word.
+__device__ __forceinline__ double exp_wide(double x) {
+  constexpr double kRound = 6755399441055744.0;
+  const double t = fma(x, 1.4426950408889634, kRound);
+  const double r = fma(kRound - t, 0.6931471805599453, x);
+  double p = 1.0 / 3628800.0;
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
+}
+
+// Order of the selection as an unsigned number: larger values first, a NaN
+// below every value.  0 is left for what cannot be selected.
+__device__ __forceinline__ uint32_t order_of(float c) {
+  const uint32_t b = __float_as_uint(c);
+  if (c != c) return 1u;
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  if (o <= 1u) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A lane's experts: chunks of CH consecutive ones, 32 CH apart, so that a warp
+// reads and writes whole 16-byte pieces of a row where N allows it.
+template <int PER>
+struct Lanes {
+  static constexpr int CH = PER < 4 ? PER : 4, Q = PER / CH;
+  static __device__ __forceinline__ int expert(int lane, int e) {
+    return (e / CH) * 32 * CH + lane * CH + e % CH;
+  }
+  static __device__ __forceinline__ void load(const float* row, int N, int lane, float fill,
+                                              float* v) {
+    if (CH == 4 && N % 4 == 0) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int j = expert(lane, q * CH);
+        float4 x = make_float4(fill, fill, fill, fill);
+        if (j < N) x = *reinterpret_cast<const float4*>(row + j);
+        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const int j = expert(lane, e);
+        v[e] = j < N ? row[j] : fill;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(float* row, int N, int lane, const float* v) {
+    if (CH == 4 && N % 4 == 0) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int j = expert(lane, q * CH);
+        if (j < N)
+          *reinterpret_cast<float4*>(row + j) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const int j = expert(lane, e);
+        if (j < N) row[j] = v[e];
+      }
+    }
+  }
+};
+
+struct SelectParams {
+  int T, N, k, renorm, sigmoid, n_group, top_group, group_top;
+  float scale;
+  const float* logits;
+  const float* bias;
+  int32_t* top_idx;
+  float* top_w;
+  float* scores;
+};
+
+// One warp per token.
+template <int PER>
+__global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_constant__ SelectParams p) {
+  using L = Lanes<PER>;
+  extern __shared__ __align__(16) float sel_mem[];  // per warp: scores [N], then (groups) c [N]
+  pdl_wait();
+  pdl_allow_next();
+  const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, N = p.N;
+  const int64_t t = (int64_t)blockIdx.x * kSelWarps + wib;
+  if (t >= p.T) return;
+  const bool groups = p.n_group > 1;
+  float* sc = sel_mem + (size_t)wib * N * (groups ? 2 : 1);
+  float* cs = sc + N;
+  float z[PER];
+  L::load(p.logits + t * N, N, lane, -INFINITY, z);
+  // scores
+  if (p.sigmoid) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      // beyond 110 the fp32 score no longer changes
+      const double x = (double)fminf(fmaxf(-z[e], -110.0f), 110.0f);
+      const float s = (float)recip(1.0 + exp_wide(x));
+      z[e] = z[e] != z[e] ? z[e] : s;
+    }
+  } else {
+    float m = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      m = fmaxf(m, z[e]);
+      nan |= z[e] != z[e];
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    nan = __any_sync(0xffffffffu, nan) || m == INFINITY;
+    double x[PER], sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      // a logit of -infinity scores 0, in a row of nothing else too
+      x[e] = z[e] == -INFINITY ? 0.0 : exp_wide(fmax((double)z[e] - (double)m, -150.0));
+      sum += x[e];
+    }
+    sum = warp_sum(sum);
+    const double r = sum > 0.0 ? recip(sum) : 0.0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) z[e] = nan ? __uint_as_float(0x7FC00000u) : (float)(x[e] * r);
+  }
+  if (p.scores) L::store(p.scores + t * N, N, lane, z);
+  // the order of the selection, and the scores for the weights
+  uint32_t ord[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int j = L::expert(lane, e);
+    ord[e] = 0u;
+    if (j < N) {
+      const float c = p.bias ? z[e] + p.bias[j] : z[e];
+      sc[j] = z[e];
+      if (groups) cs[j] = c;
+      ord[e] = order_of(c);
+    }
+  }
+  __syncwarp();
+  if (groups) {
+    // sub lanes of a group read its experts in turn and keep the two best
+    const int G = p.n_group, per = N / G;
+    int sub = 32;
+    while (sub * G > 32) sub >>= 1;
+    const int g = lane / sub;
+    uint32_t b1 = 0u, b2 = 0u;
+    if (g < G) {
+      for (int i = lane % sub; i < per; i += sub) {
+        const uint32_t o = order_of(cs[g * per + i]);
+        b2 = max(b2, min(b1, o));
+        b1 = max(b1, o);
+      }
+    }
+    for (int o = sub >> 1; o >= 1; o >>= 1) {
+      const uint32_t o1 = __shfl_xor_sync(0xffffffffu, b1, o);
+      const uint32_t o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+      b2 = max(min(b1, o1), max(b2, o2));
+      b1 = max(b1, o1);
+    }
+    const uint32_t mine =
+        order_of(p.group_top == 1 ? value_of(b1) : value_of(b1) + value_of(b2));
+    int rank = 0;
+    for (int h = 0; h < G; ++h) {
+      const uint32_t o = __shfl_sync(0xffffffffu, mine, h * sub);
+      rank += o > mine || (o == mine && h < g);
+    }
+    const uint32_t kept = __ballot_sync(0xffffffffu, g < G && rank < p.top_group);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int j = L::expert(lane, e);
+      if (j < N && !((kept >> (j / per * sub)) & 1u)) ord[e] = 0u;
+    }
+  }
+  // the k best, one at a time: the largest order, then the lowest expert of it
+  uint32_t best = 0u;
+  int at = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e)
+    if (ord[e] > best) best = ord[e], at = e;
+  int mine = 0;
+  for (int s = 0; s < p.k; ++s) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int j = best == top ? L::expert(lane, at) : INT32_MAX;
+    const int w = __reduce_min_sync(0xffffffffu, j);
+    if (lane == s) mine = w;
+    if (j == w) {  // this lane's is taken
+      best = 0u;
+      int next = 0;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        if (e == at) ord[e] = 0u;
+        if (ord[e] > best) best = ord[e], next = e;
+      }
+      at = next;
+    }
+  }
+  float a = lane < p.k ? sc[mine] : 0.0f;
+  if (p.renorm) {
+    const float S = warp_sum(a);
+    a = S == 0.0f ? 0.0f : a / S;  // nothing but zero scores: no weight
+  }
+  if (lane < p.k) {
+    p.top_idx[t * p.k + lane] = mine;
+    p.top_w[t * p.k + lane] = a * p.scale;
+  }
+}
+
+struct SelectBwdParams {
+  int T, N, k, renorm, sigmoid;
+  float scale;
+  const float* logits;
+  const int32_t* top_idx;
+  const float* d_top_w;
+  const float* d_scores;
+  float* dz;
+  int* status;
+};
+
+// One warp per token.  With g_j = dL/ds_j (d_scores plus what the weights of
+// the selected experts give):
+//   renorm: dL/ds_i = scale (da_i - sum_l da_l s_l / S) / S;  else scale da_i
+//   sigmoid: dz_j = g_j s_j (1 - s_j);  softmax: dz_j = s_j (g_j - sum g s)
+template <int PER>
+__global__ void __launch_bounds__(32 * kSelWarps)
+    route_select_bwd(const __grid_constant__ SelectBwdParams p) {
+  using L = Lanes<PER>;
+  extern __shared__ __align__(16) float sel_mem[];  // per warp: s [N], g [N]
+  pdl_wait();
+  pdl_allow_next();
+  const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, N = p.N;
+  const int64_t t = (int64_t)blockIdx.x * kSelWarps + wib;
+  if (t >= p.T) return;
+  float* ss = sel_mem + (size_t)wib * N * 2;
+  float* gs = ss + N;
+  float z[PER], f[PER];
+  L::load(p.logits + t * N, N, lane, -INFINITY, z);
+  if (p.sigmoid) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {  // s, and 1 - s without cancellation
+      const float x = expf(-fabsf(z[e]));
+      const float r = 1.0f / (1.0f + x);
+      f[e] = z[e] >= 0.0f ? x * r : r;
+      z[e] = z[e] >= 0.0f ? r : x * r;
+    }
+  } else {
+    float m = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) m = fmaxf(m, z[e]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      z[e] = z[e] == -INFINITY ? 0.0f : expf(z[e] - m);
+      sum += z[e];
+    }
+    sum = warp_sum(sum);
+    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) z[e] *= r;
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int j = L::expert(lane, e);
+    if (j < N) ss[j] = z[e], gs[j] = 0.0f;
+  }
+  __syncwarp();
+  // the selected experts' part; an index that is there twice counts twice
+  int idx = lane < p.k ? p.top_idx[t * p.k + lane] : -1;
+  float da = lane < p.k ? p.d_top_w[t * p.k + lane] : 0.0f;
+  if (lane < p.k && (idx < 0 || idx >= N)) {
+    record_error(p.status, MOE_ERR_BOUNDS);
+    idx = -1;
+    da = 0.0f;
+  }
+  const float s = idx >= 0 ? ss[idx] : 0.0f;
+  da *= p.scale;
+  if (p.renorm) {
+    const float S = warp_sum(s), ds = warp_sum(da * s);
+    da = S == 0.0f || idx < 0 ? 0.0f : (da - ds / S) / S;
+  }
+  float sum = 0.0f;
+  int first = 32;
+  for (int r = 0; r < p.k; ++r) {
+    const int ir = __shfl_sync(0xffffffffu, idx, r);
+    const float dr = __shfl_sync(0xffffffffu, da, r);
+    if (ir == idx) {
+      sum += dr;
+      first = min(first, r);
+    }
+  }
+  if (idx >= 0 && first == lane) gs[idx] = sum;
+  __syncwarp();
+  float g[PER];
+  if (p.d_scores) {
+    L::load(p.d_scores + t * N, N, lane, 0.0f, g);
+  } else {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) g[e] = 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int j = L::expert(lane, e);
+    if (j < N) g[e] += gs[j];
+  }
+  if (p.sigmoid) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) g[e] *= z[e] * f[e];
+  } else {
+    float dot = 0.0f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) dot = fmaf(g[e], z[e], dot);
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) g[e] = z[e] * (g[e] - dot);
+  }
+  L::store(p.dz + t * N, N, lane, g);
+}
+
+template <template <int> class K, typename P>
+int by_width(const P& p, size_t smem, cudaStream_t st) {
+  const int chunks = (p.N + 127) / 128;  // of 4 experts a lane
+  if (p.N <= 32) return K<1>::launch(p, smem, st);
+  if (p.N <= 64) return K<2>::launch(p, smem, st);
+  switch (chunks) {
+    case 1: return K<4>::launch(p, smem, st);
+    case 2: return K<8>::launch(p, smem, st);
+    case 3: return K<12>::launch(p, smem, st);
+    case 4: return K<16>::launch(p, smem, st);
+    case 5: return K<20>::launch(p, smem, st);
+    case 6: return K<24>::launch(p, smem, st);
+    case 7: return K<28>::launch(p, smem, st);
+    default: return K<32>::launch(p, smem, st);
+  }
+}
+
+template <int PER>
+struct Select {
+  static int launch(const SelectParams& p, size_t smem, cudaStream_t st) {
+    MOE_PREFER_SHARED((route_select<PER>));
+    launch_pdl(route_select<PER>, dim3((unsigned)((p.T + kSelWarps - 1) / kSelWarps)),
+               dim3(32 * kSelWarps), smem, st, p);
+    return launch_status();
+  }
+};
+template <int PER>
+struct SelectBwd {
+  static int launch(const SelectBwdParams& p, size_t smem, cudaStream_t st) {
+    MOE_PREFER_SHARED((route_select_bwd<PER>));
+    launch_pdl(route_select_bwd<PER>, dim3((unsigned)((p.T + kSelWarps - 1) / kSelWarps)),
+               dim3(32 * kSelWarps), smem, st, p);
+    return launch_status();
+  }
+};
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool gating_ok(const moe_shape* s, const moe_gating* g) {
+  if (!s || !g || s->T < 0 || s->N <= 0 || s->N > 1024 || s->k <= 0 || s->k > 32 || s->k > s->N)
+    return false;
+  if ((int64_t)s->T * s->k >= (int64_t)1 << 31) return false;
+  if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) return false;
+  if (g->n_group < 1 || g->n_group > 32 || s->N % g->n_group != 0) return false;
+  const int per = s->N / g->n_group;
+  if (g->group_top < 1 || g->group_top > 2 || g->group_top > per) return false;
+  return g->top_group >= 1 && g->top_group <= g->n_group && (int64_t)g->top_group * per >= s->k;
+}
+
+int launch_select(const moe_shape& s, const moe_gating& g, const float* logits, const float* bias,
+                  int32_t* top_idx, float* top_w, float* scores, cudaStream_t st) {
+  if (s.T == 0) return MOE_OK;
+  SelectParams p{s.T, s.N, s.k, s.renorm, g.score == MOE_SCORE_SIGMOID, g.n_group, g.top_group,
+                 g.group_top, g.scale, logits, bias, top_idx, top_w, scores};
+  // every group kept is no limit
+  if (g.top_group == g.n_group) p.n_group = 1;
+  return by_width<Select>(p, (size_t)kSelWarps * s.N * 4 * (p.n_group > 1 ? 2 : 1), st);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_route_select(const moe_shape* shape, const moe_gating* gating,
+                                const float* logits, const float* bias, int32_t* top_idx,
+                                float* top_w, float* scores, void* stream) {
+  using namespace moe;
+  if (!gating_ok(shape, gating)) return MOE_ERR_INVALID_ARG;
+  if (shape->T > 0 && (!logits || !top_idx || !top_w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(scores) || !aligned4(bias) || !aligned4(top_idx) ||
+      !aligned4(top_w))
+    return MOE_ERR_INVALID_ARG;
+  return launch_select(*shape, *gating, logits, bias, top_idx, top_w, scores, as_stream(stream));
+}
+
+extern "C" int moe_route_select_bwd(const moe_shape* shape, const moe_gating* gating,
+                                    const float* logits, const int32_t* top_idx,
+                                    const float* d_top_w, const float* d_scores, float* dz,
+                                    void* stream) {
+  using namespace moe;
+  if (!gating_ok(shape, gating)) return MOE_ERR_INVALID_ARG;
+  const moe_shape& s = *shape;
+  if (s.T > 0 && (!logits || !top_idx || !d_top_w || !dz)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(d_scores) || !aligned16(dz) || !aligned4(top_idx) ||
+      !aligned4(d_top_w))
+    return MOE_ERR_INVALID_ARG;
+  if (s.T == 0) return MOE_OK;
+  SelectBwdParams p{s.T, s.N, s.k, s.renorm, gating->score == MOE_SCORE_SIGMOID, gating->scale,
+                    logits, top_idx, d_top_w, d_scores, dz, status_word()};
+  return by_width<SelectBwd>(p, (size_t)kSelWarps * s.N * 8, as_stream(stream));
+}
+
+extern "C" size_t moe_route_scored_workspace_bytes(const moe_shape* shape) {
+  if (!moe::shape_ok(shape)) return 0;
+  return moe::route_ws_bytes(*shape);
+}
+
+extern "C" int moe_route_scored(const moe_shape* shape, const moe_gating* gating, const void* u,
+                                int32_t u_dtype, const float* w_route, const float* bias,
+                                int32_t* top_idx, float* top_w, float* scores, float* logits,
+                                void* ws, size_t ws_bytes, void* stream) {
+  using namespace moe;
+  if (!shape_ok(shape) || !gating_ok(shape, gating) || !valid_act_dtype(u_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (shape->T > 0 && (!u || !w_route || !top_idx || !top_w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(u) || !aligned16(w_route) || !aligned16(logits) || !aligned16(scores) ||
+      !aligned4(bias) || !aligned4(top_idx) || !aligned4(top_w))
+    return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0) return MOE_OK;
+  if (!logits && (!ws || ws_bytes < route_ws_bytes(*shape))) return MOE_ERR_WORKSPACE;
+  if (!logits && !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  float* z = logits ? logits : static_cast<float*>(ws);
+  cudaStream_t st = as_stream(stream);
+  const int rc = launch_route_logits(*shape, u, u_dtype, w_route, nullptr, z, st);
+  if (rc != MOE_OK) return rc;
+  return launch_select(*shape, *gating, z, bias, top_idx, top_w, scores, st);
+}

@@ -89,9 +89,9 @@ struct TcParams {
   int out_ld;             // elements per output row
   int out_col_group;      // output column offset per group (groups sharing tokens)
   int* status;
-  // E4M3 operands only: fp32 scale per row of A (gate/up mode: gate rows in
-  // a_scale[0], up rows in a_scale[1]); the operand value is
-  // scale * e4m3(code).  b_scale (nullable): a factor per row of B, the
+  // E4M3 and 8-bit integer operands: fp32 scale per row of A (gate/up mode:
+  // gate rows in a_scale[0], up rows in a_scale[1]); the operand value is
+  // scale * code.  b_scale (nullable): a factor per row of B, the
   // token rows (E4M3 token scales, or the combine weight a of each grouped
   // row, so the down GEMM stores a * F(u)).
   const float* a_scale[2];
@@ -118,13 +118,19 @@ struct Layout {
   }
 };
 
-// F8: E4M3 A and B (tcgen05 kind::f8f6f4), 128 codes per 128-byte k-block,
-// row scales applied in the epilogue; gate/up mode then stores H as E4M3
-// codes with no scale.  Otherwise bf16 A and B (kind::f16).
-template <int BN, int S, int ACT, int CG, bool F8>
+// KIND picks A and B:
+//   OPS_BF16  kind::f16
+//   OPS_E4M3  kind::f8f6f4, 128 codes per 128-byte k-block, row scales applied
+//             in the epilogue; gate/up mode then stores H as E4M3 codes with
+//             no scale
+//   OPS_I8    kind::i8, 128 codes per 128-byte k-block, exact s32 sums, row
+//             scales applied to the sums' fp32 values; gate/up mode stores H
+//             as bf16
+template <int BN, int S, int ACT, int CG, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_constant__ TcParams p) {
   using L = Layout<BN, S, CG>;
-  constexpr int KE = F8 ? 2 * kBK : kBK;  // elements per 128-byte k-block
+  constexpr bool F8 = KIND == OPS_E4M3, I8 = KIND == OPS_I8;
+  constexpr int KE = F8 || I8 ? 2 * kBK : kBK;  // elements per 128-byte k-block
   static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair per MMA");
   // pair geometry: rank 0 issues the MMAs of the pair; tiles are per pair
   const uint32_t rank = CG == 2 ? tc::cluster_rank() : 0u;
@@ -229,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
   const int total_tiles = grp_pre[p.G];
   const int kblocks = p.seg_end[p.nseg - 1];
 
-  // n_mma: MMA width of a tile with n_valid token columns (multiple of 16)
-  auto mma_width = [&](int n_valid) { return (n_valid + 15) & ~15; };
+  // n_mma: MMA width of a tile with n_valid token columns (a multiple of 16,
+  // of 32 for kind::i8)
+  auto mma_width = [&](int n_valid) { return I8 ? (n_valid + 31) & ~31 : (n_valid + 15) & ~15; };
   auto decode = [&](int tile, int& g, int& m, int& n) {
     int lo = 0, hi = p.G;
     while (hi - lo > 1) {
@@ -333,8 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
         decode(tile, g, m, n);
         const int n_valid = min(BN, grp_cnt[g] - n * BN);
         const uint32_t n_mma = (uint32_t)mma_width(n_valid);
-        const uint32_t idesc = F8 ? tc::idesc_e4m3_f32(CG * kBM, n_mma)
-                                  : tc::idesc_bf16_f32(CG * kBM, n_mma);
+        const uint32_t idesc = F8   ? tc::idesc_e4m3_f32(CG * kBM, n_mma)
+                               : I8 ? tc::idesc_i8_s32(CG * kBM, n_mma)
+                                    : tc::idesc_bf16_f32(CG * kBM, n_mma);
         const int b = it & 1;
         const uint32_t use = (uint32_t)(it >> 1);
         if (!tc::mbar_wait(tc::smem_u32(&tempty[b]), (use & 1u) ^ 1u, abort_flag, kWaitBudget)) {
@@ -359,6 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
             if (F8) {
               if (CG == 2) tc::mma_e4m3_pair(d_tmem, ad, bd, idesc, acc);
               else tc::mma_e4m3(d_tmem, ad, bd, idesc, acc);
+            } else if (I8) {
+              if (CG == 2) tc::mma_i8_pair(d_tmem, ad, bd, idesc, acc);
+              else tc::mma_i8(d_tmem, ad, bd, idesc, acc);
             } else {
               if (CG == 2) tc::mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
               else tc::mma_bf16(d_tmem, ad, bd, idesc, acc);
@@ -428,21 +439,26 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
       }
       tc::tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
-      // E4M3: this thread's weight-row scale (gate/up: its TMEM row is a
-      // gate row in lanes 0-63, an up row in lanes 64-127)
+      // E4M3, 8-bit integers: this thread's weight-row scale (gate/up: its
+      // TMEM row is a gate row in lanes 0-63, an up row in lanes 64-127)
       float w_scale = 1.0f;
-      if (F8) {
+      if (F8 || I8) {
         if (p.mode == MODE_GATEUP) {
           const int hid = g * p.a_rows_per_group + (m * CG + (int)rank) * 64 + (row & 63);
           w_scale = p.a_scale[row >> 6][hid];
         } else {
-          w_scale = p.a_scale[0][g * p.a_rows_per_group + (m * CG + (int)rank) * kBM + row];
+          const int a = (m * CG + (int)rank) * kBM + row;  // the last tile may pass the group's rows
+          if (a < p.a_rows_per_group) w_scale = p.a_scale[0][g * p.a_rows_per_group + a];
         }
       }
       for (int c = 0; c < n_valid; c += 32) {
         float v[32];
         tc::tmem_ld_32x32b_x32(t_row + (uint32_t)c, v);
-        if (F8 || p.b_scale) {  // row scales of A (E4M3) and of B (E4M3, or combine weights)
+        if (I8) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(__float_as_int(v[j]));
+        }
+        if (F8 || I8 || p.b_scale) {  // row scales of A and of B (codes, or combine weights)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = v[j] * w_scale * (p.b_scale ? fac[c + j] : 1.0f);
         }
@@ -479,17 +495,27 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
           }
           named_sync_epi();
         } else {
-          const int col = g * p.out_col_group + (m * CG + (int)rank) * kBM + row;
-          if (p.mode == MODE_STORE_F32) {
+          const int a = (m * CG + (int)rank) * kBM + row;
+          const int col = g * p.out_col_group + a;
+          // 8-bit integers take any number of output columns: the last tile
+          // may pass them, its extra weight rows are another group's or zeros
+          const int stored = !I8 || a < p.a_rows_per_group ? n_valid : 0;
+          if (I8 && p.mode == MODE_STORE_F16) {
+            __half* o = static_cast<__half*>(p.out);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < stored)
+                o[(size_t)(tok0 + c + j) * p.out_ld + col] = __float2half_rn(v[j]);
+          } else if (p.mode == MODE_STORE_F32) {
             float* o = static_cast<float*>(p.out);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c + j < n_valid) o[(size_t)(tok0 + c + j) * p.out_ld + col] = v[j];
+              if (c + j < stored) o[(size_t)(tok0 + c + j) * p.out_ld + col] = v[j];
           } else {
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c + j < n_valid)
+              if (c + j < stored)
                 o[(size_t)(tok0 + c + j) * p.out_ld + col] = __float2bfloat16_rn(v[j]);
           }
         }
@@ -585,10 +611,10 @@ int resident_pairs(Kernel kernel, size_t smem, int dev) {
   return n;
 }
 
-template <int BN, int S, int ACT, int CG, bool F8>
+template <int BN, int S, int ACT, int CG, int KIND>
 int launch_tc(const TcParams& p, int64_t units_upper, cudaStream_t st) {
   using L = Layout<BN, S, CG>;
-  auto kernel = tc_grouped_gemm<BN, S, ACT, CG, F8>;
+  auto kernel = tc_grouped_gemm<BN, S, ACT, CG, KIND>;
   const size_t smem = L::bytes(p.G);
   static std::atomic<bool> configured[kMaxDevices];
   int dev = 0;
@@ -600,7 +626,7 @@ int launch_tc(const TcParams& p, int64_t units_upper, cudaStream_t st) {
       return MOE_ERR_CUDA;
     mark_setup(configured, dev);
   }
-  MOE_PREFER_SHARED((tc_grouped_gemm<BN, S, ACT, CG, F8>));
+  MOE_PREFER_SHARED((tc_grouped_gemm<BN, S, ACT, CG, KIND>));
   if (units_upper <= 0) return MOE_OK;
   if (CG == 1) {
     int64_t grid = sm_count();
@@ -639,27 +665,28 @@ int pick_bn(int m_tiles, int64_t max_rows, int G, int cg) {
   return up256 >= 2LL * sm_count() / cg ? 256 : 128;
 }
 
-template <bool F8>
+template <int KIND>
 int launch_tc_typed(const TcParams& p, int64_t upper, int bn, int cg, cudaStream_t st) {
   const bool situ = p.mode == MODE_GATEUP && p.act_kind == MOE_ACT_SITU_GLU;
   if (cg == 2) {
     if (bn == 256)
-      return situ ? launch_tc<256, 6, MOE_ACT_SITU_GLU, 2, F8>(p, upper, st)
-                  : launch_tc<256, 6, MOE_ACT_SWIGLU, 2, F8>(p, upper, st);
-    return situ ? launch_tc<128, 8, MOE_ACT_SITU_GLU, 2, F8>(p, upper, st)
-                : launch_tc<128, 8, MOE_ACT_SWIGLU, 2, F8>(p, upper, st);
+      return situ ? launch_tc<256, 6, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
+                  : launch_tc<256, 6, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st);
+    return situ ? launch_tc<128, 8, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
+                : launch_tc<128, 8, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st);
   }
   if (bn == 256)
-    return situ ? launch_tc<256, 4, MOE_ACT_SITU_GLU, 1, F8>(p, upper, st)
-                : launch_tc<256, 4, MOE_ACT_SWIGLU, 1, F8>(p, upper, st);
-  return situ ? launch_tc<128, 6, MOE_ACT_SITU_GLU, 1, F8>(p, upper, st)
-              : launch_tc<128, 6, MOE_ACT_SWIGLU, 1, F8>(p, upper, st);
+    return situ ? launch_tc<256, 4, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
+                : launch_tc<256, 4, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st);
+  return situ ? launch_tc<128, 6, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
+              : launch_tc<128, 6, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st);
 }
 
-int launch_tc_bn(const TcParams& p, int64_t max_rows, int bn, int cg, bool f8, cudaStream_t st) {
+int launch_tc_bn(const TcParams& p, int64_t max_rows, int bn, int cg, int kind, cudaStream_t st) {
   const int64_t upper = (int64_t)p.m_tiles * ((max_rows + bn - 1) / bn + p.G);
-  return f8 ? launch_tc_typed<true>(p, upper, bn, cg, st)
-            : launch_tc_typed<false>(p, upper, bn, cg, st);
+  return kind == OPS_E4M3 ? launch_tc_typed<OPS_E4M3>(p, upper, bn, cg, st)
+         : kind == OPS_I8 ? launch_tc_typed<OPS_I8>(p, upper, bn, cg, st)
+                          : launch_tc_typed<OPS_BF16>(p, upper, bn, cg, st);
 }
 
 }  // namespace
@@ -692,6 +719,7 @@ int tc_gateup(const int32_t* offsets, int T, int G, const void* X, int64_t x_row
               const void* w_gate, const void* w_up, int hidden, const moe_act& act, void* out,
               int out_ld, int out_col_group, cudaStream_t st, const TcF8* f8) {
   if (f8 && K % (2 * kBK) != 0) return MOE_ERR_UNSUPPORTED;
+  const int kind = f8 ? f8->kind : OPS_BF16;
   TcParams p{};
   const int64_t rows_w = (int64_t)G * hidden;
   const int64_t max_rows = offsets ? x_rows : (int64_t)T * G;
@@ -725,7 +753,7 @@ int tc_gateup(const int32_t* offsets, int T, int G, const void* X, int64_t x_row
   p.out_ld = out_ld;
   p.out_col_group = out_col_group;
   p.status = status_word();
-  return launch_tc_bn(p, max_rows, bn, cg, u8, st);
+  return launch_tc_bn(p, max_rows, bn, cg, kind, st);
 }
 
 // Plain GEMM over 1..3 K-segments accumulated into one output:
@@ -734,14 +762,17 @@ int tc_store(const int32_t* offsets, int T, int G, int m_rows, const TcSeg* segs
              void* out, int mode, int out_ld, cudaStream_t st, const TcF8* f8,
              const float* b_row_scale) {
   if (nseg < 1 || nseg > kMaxSeg) return MOE_ERR_INVALID_ARG;
-  if (f8 && (nseg != 1 || segs[0].K % (2 * kBK) != 0)) return MOE_ERR_UNSUPPORTED;
+  const int kind = f8 ? f8->kind : OPS_BF16;
+  const bool i8 = kind == OPS_I8;
+  if (f8 && (nseg != 1 || (!i8 && segs[0].K % (2 * kBK) != 0))) return MOE_ERR_UNSUPPORTED;
   const bool u8 = f8 != nullptr;
   const int ke = u8 ? 2 * kBK : kBK;
   TcParams p{};
   const int64_t max_rows = offsets ? segs[0].b_rows : (int64_t)T * G;
-  // CTA pairs take 256 output rows (128 per CTA) per tile
-  const int cg = m_rows % (2 * kBM) == 0 ? 2 : 1;
-  const int m_tiles = m_rows / (kBM * cg);
+  // CTA pairs take 256 output rows (128 per CTA) per tile; for 8-bit integers
+  // the last tile may be ragged (and the last k-block: the loads fill zeros)
+  const int cg = i8 ? (m_rows > kBM ? 2 : 1) : m_rows % (2 * kBM) == 0 ? 2 : 1;
+  const int m_tiles = (m_rows + kBM * cg - 1) / (kBM * cg);
   const int bn = pick_bn(m_tiles, max_rows, G, cg);
   // distinct (pointer, rows, cols, box) tensor maps, at most four
   const void* key_p[4];
@@ -767,7 +798,7 @@ int tc_store(const int32_t* offsets, int T, int G, int m_rows, const TcSeg* segs
     if (ia < 0 || ib < 0) return MOE_ERR_CUDA;
     p.amap[i] = ia;
     p.bmap[i] = ib;
-    kb += segs[i].K / ke;
+    kb += (segs[i].K + ke - 1) / ke;
     p.seg_end[i] = kb;
     p.arow[i] = segs[i].arow;
     p.bcol[i] = segs[i].bcol;
@@ -789,7 +820,7 @@ int tc_store(const int32_t* offsets, int T, int G, int m_rows, const TcSeg* segs
     p.a_scale[0] = f8->a_scale[0];
     p.b_scale = f8->b_scale;
   }
-  return launch_tc_bn(p, max_rows, bn, cg, u8, st);
+  return launch_tc_bn(p, max_rows, bn, cg, kind, st);
 }
 
 }  // namespace moe

@@ -485,6 +485,18 @@ size_t route_ws_bytes(const moe_shape& s) { return align_up((size_t)s.T * s.N * 
 
 int route_tokens_per_block(int N) { return kRouteThreads / (N <= 8 ? 8 : 16); }
 
+int launch_route_logits(const moe_shape& s, const void* u, int32_t u_dtype, const float* w_route,
+                        const float* bias, float* z, cudaStream_t st) {
+  if (u_dtype == MOE_F32) {
+    launch_logits(static_cast<const float*>(u), w_route, bias, z, s.T, s.d, s.N, st);
+  } else if (u_dtype == MOE_BF16) {
+    launch_logits(static_cast<const __nv_bfloat16*>(u), w_route, bias, z, s.T, s.d, s.N, st);
+  } else {
+    launch_logits(static_cast<const __half*>(u), w_route, bias, z, s.T, s.d, s.N, st);
+  }
+  return launch_status();
+}
+
 int launch_route(const moe_shape& s, const void* u, int32_t u_dtype, const float* w_route,
                  const float* bias, int32_t* top_idx, float* top_w, float* probs, float* logits,
                  void* ws, cudaStream_t st, int32_t* hist) {
@@ -511,13 +523,8 @@ int launch_route(const moe_shape& s, const void* u, int32_t u_dtype, const float
     return launch_status();
   }
   float* z = logits ? logits : static_cast<float*>(ws);
-  if (u_dtype == MOE_F32) {
-    launch_logits(static_cast<const float*>(u), w_route, bias, z, s.T, s.d, s.N, st);
-  } else if (u_dtype == MOE_BF16) {
-    launch_logits(static_cast<const __nv_bfloat16*>(u), w_route, bias, z, s.T, s.d, s.N, st);
-  } else {
-    launch_logits(static_cast<const __half*>(u), w_route, bias, z, s.T, s.d, s.N, st);
-  }
+  const int rc = launch_route_logits(s, u, u_dtype, w_route, bias, z, st);
+  if (rc != MOE_OK) return rc;
   const int blocks = (s.T + 7) / 8;
   const int per = (s.N + 31) / 32;
 #define MOE_TOPK(P)                                                                          \

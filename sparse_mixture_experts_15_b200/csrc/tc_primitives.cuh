@@ -217,6 +217,27 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
+// Signed 8-bit integer forms (kind::i8, s32 accumulate): K = 32 codes
+// (32 bytes) per instruction, every sum exact.
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor: K-major tile, 128-byte swizzle, rows of
 // 128 bytes in 8-row (1024-byte) atoms.  Fields: start address >> 4 [0,14),
 // leading byte offset >> 4 [16,30) (unused for swizzled K-major, set to 1),
@@ -242,6 +263,14 @@ __device__ __forceinline__ uint32_t idesc_bf16_f32(uint32_t M, uint32_t N) {
 // (format 0 at [7,10) and [10,13)), both K-major, N >> 3, M >> 4.
 __device__ __forceinline__ uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Instruction descriptor of kind::i8: D s32 [4,6)=2, A and B signed 8-bit
+// (format 1 at [7,10) and [10,13)), both K-major, no saturation, N >> 3,
+// M >> 4.  N is a multiple of 32 here: every such N up to 256 is allowed for
+// M = 128 on one CTA and M = 256 on a pair.
+__device__ __forceinline__ uint32_t idesc_i8_s32(uint32_t M, uint32_t N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 }  // namespace tc
