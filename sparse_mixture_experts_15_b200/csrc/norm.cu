@@ -9,7 +9,9 @@
 namespace moe {
 namespace {
 
-constexpr int kFwdCtas = 3;  // CTAs per SM
+// CTAs per SM (three, of 80 registers a thread, spill and take 59 us where two
+// take 45: 8192 x 4096 bf16, both norms)
+constexpr int kFwdCtas = 2;
 
 struct NormFwd {
   int T, d, C;             // C: CTAs of a cluster, each with its share of a row's columns
@@ -18,6 +20,7 @@ struct NormFwd {
   const float *w_post, *w_pre, *gate_ch, *gate_tok;
   float alpha, beta, eps, inv_d;
   void *x_out, *u;
+  int* status;
 };
 
 // HASY: a block's output comes in (POST: normed first; FULL: gated by element;
@@ -25,122 +28,131 @@ struct NormFwd {
 template <typename T, int S, bool HASY, bool POST, bool FULL, bool PRE>
 __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
     block_norm_fwd(const __grid_constant__ NormFwd p) {
-  extern __shared__ __align__(16) char fifo_mem[];
+  extern __shared__ __align__(128) char ring_mem[];
   __shared__ SumBuffers sum_mem;
+  __shared__ uint64_t full_bar[kMaxTeams][S];
+  constexpr int W = chunk_width<T, T>(), NV = kCols / W, E = sizeof(T), A = 1 + HASY + FULL;
+  const int nt = p.nt;
+  const Place q = place_of(nt, p.C, p.d, p.T);
+  RowSum sums{&sum_mem, q.team, nt, nt / 32, p.C, 0};
+  const uint32_t slot = nt * kCols * E;  // bytes of an array in a stage
+  const uint32_t ring = smem_addr(ring_mem) + q.team * S * A * slot;
+  const uint32_t bar = smem_addr(full_bar[q.team]);
+  const bool leader = q.lane_t == 0;
+  if (leader) {
+    for (int s = 0; s < S; ++s) tc::mbar_init(bar + 8 * s, 1);
+    tc::fence_barrier_init();
+  }
+  for (int s = 0; s < S * A; ++s) zero_tail(q, nt, ring + s * slot, E);
+  team_sync(q.team, nt);
+  if (p.C > 1) cluster_barrier();  // every CTA of the cluster runs before its memory is written
   pdl_wait();
   pdl_allow_next();
-  const Place q = place_of(p.nt, p.C, p.d, p.T);
-  RowSum sums{&sum_mem, q.team, p.nt, p.nt / 32, p.C, 0};
-  if (p.C > 1) cluster_barrier();  // every CTA of the cluster runs before its memory is written
-  constexpr int P = planes<T>();
-  const uint32_t step = blockDim.x * 16, stage = P * (1 + HASY + FULL) * step;
-  const uint32_t base = smem_addr(fifo_mem + threadIdx.x * 16);
-  const size_t skip = (size_t)q.step * p.d;
-  Stream<T> sx, sy, sg;
-  sx.start(p.x, q, p.d, 0);
-  if (HASY) sy.start(p.y, q, p.d, P);
-  if (FULL) sg.start(p.gate_full, q, p.d, 2 * P);
-  int uncopied = q.count;
-  auto issue = [&](uint32_t at) {
-    if (uncopied > 0) {
-      sx.copy(q, at, step, skip);
-      if (HASY) sy.copy(q, at, step, skip);
-      if (FULL) sg.copy(q, at, step, skip);
-      --uncopied;
-    }
-    cp_commit();
+  auto issue = [&](uint32_t row, int s) {  // by the leader
+    const size_t e = (size_t)row * (uint32_t)p.d + q.begin;
+    const uint32_t at = ring + s * A * slot, bytes = q.cols * E;
+    tc::mbar_arrive_expect_tx(bar + 8 * s, A * bytes);
+    if (bytes == 0) return;
+    bulk_copy(at, static_cast<const T*>(p.x) + e, bytes, bar + 8 * s);
+    if (HASY) bulk_copy(at + slot, static_cast<const T*>(p.y) + e, bytes, bar + 8 * s);
+    if (FULL)
+      bulk_copy(at + 2 * slot, static_cast<const T*>(p.gate_full) + e, bytes, bar + 8 * s);
   };
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(base + s * stage);
+  if (leader)
+    for (int s = 0; s < S && s < q.count; ++s) issue(q.first + s * q.step, s);
   Pair coef[8], wpre[8];  // out_scale times the post gain and a channel gate
-  if (HASY) gains(q, p.w_post, p.gate_ch, p.beta, coef);
-  if (PRE) gains(q, p.w_pre, nullptr, 1.0f, wpre);
+  if (HASY) gains<W>(q, nt, p.w_post, p.gate_ch, p.beta, coef);
+  if (PRE) gains<W>(q, nt, p.w_pre, nullptr, 1.0f, wpre);
   const Pair alpha = pair(p.alpha, p.alpha);
-  T* xo = static_cast<T*>(p.x_out) + (size_t)q.first * p.d;
-  T* u = static_cast<T*>(p.u) + (size_t)q.first * p.d;
-  uint32_t at = base, last = base + (S - 1) * stage;  // this row's stage, the one before it
+  const uint32_t mine = q.lane_t * W * E, next = nt * W * E;  // this thread's first chunk, its step
   uint32_t t = q.first;
-  for (int left = q.count; left > 0; --left, t += q.step) {
-    issue(last);
+  Ring at_row{bar, S, 0, 0, true, 0, 0};
+  for (int i = 0; i < q.count; ++i, t += q.step) {
     float r = 1.0f;
     if (HASY && p.gate_tok) r = p.gate_tok[t];
-    cp_wait<S - 1>();
-    Pair x[8];
+    at_row.wait(p.status);
+    const int s = at_row.s;
+    const uint32_t at = ring + s * A * slot + mine;
+    Pair x[8], y[8], g[8];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) sx.get(v, at, step, x + 4 * v);
+    for (int v = 0; v < NV; ++v) {
+      get<W, T>(at + v * next, x + v * W / 2);
+      if (HASY) get<W, T>(at + slot + v * next, y + v * W / 2);
+      if (FULL) get<W, T>(at + 2 * slot + v * next, g + v * W / 2);
+    }
+    const size_t e = (size_t)t * (uint32_t)p.d + q.begin + q.lane_t * W;
     if (HASY) {
-      Pair y[8];
-#pragma unroll
-      for (int v = 0; v < 2; ++v) sy.get(v, at, step, y + 4 * v);
       if (POST) {
         Pair a = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a = fma2(y[i], y[i], a);
+        for (int k = 0; k < 8; ++k) a = fma2(y[k], y[k], a);
         float ss[1] = {sum2(a)};
         row_sum<1>(sums, ss);
         r *= rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
       }
       const Pair rr = pair(r, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = mul2(y[i], rr);
-      if (FULL) {
-        Pair g[4];
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          sg.get(v, at, step, g);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[4 * v + i] = mul2(y[4 * v + i], g[i]);
-        }
+      for (int k = 0; k < 8; ++k) {
+        y[k] = mul2(y[k], rr);
+        if (FULL) y[k] = mul2(y[k], g[k]);
+        x[k] = fma2(y[k], coef[k], mul2(x[k], alpha));
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fma2(y[i], coef[i], mul2(x[i], alpha));
       // rounded here: the next norm reads the stream as it is stored
 #pragma unroll
-      for (int v = 0; v < 2; ++v) store_chunk<T>(xo + q.c[v], q.on[v], x + 4 * v);
-      xo += skip;
+      for (int v = 0; v < NV; ++v)
+        put<W>(static_cast<T*>(p.x_out) + e + v * nt * W, (v * nt + q.lane_t) * W < q.cols,
+               x + v * W / 2);
     }
     if (PRE) {
       Pair a = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a = fma2(x[i], x[i], a);
+      for (int k = 0; k < 8; ++k) a = fma2(x[k], x[k], a);
       float ss[1] = {sum2(a)};
       row_sum<1>(sums, ss);
       const float r1 = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
       const Pair rr = pair(r1, r1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(x[i], rr), wpre[i]);
+      for (int k = 0; k < 8; ++k) x[k] = mul2(mul2(x[k], rr), wpre[k]);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) store_chunk<T>(u + q.c[v], q.on[v], x + 4 * v);
-      u += skip;
+      for (int v = 0; v < NV; ++v)
+        put<W>(static_cast<T*>(p.u) + e + v * nt * W, (v * nt + q.lane_t) * W < q.cols,
+               x + v * W / 2);
     }
-    last = at;
-    at = at == base + (S - 1) * stage ? base : at + stage;
+    // every thread of the team has read the row: the sums' barriers came after
+    if (!POST && !PRE) team_sync(q.team, nt);
+    if (nt == 32) __syncwarp();
+    if (leader && at_row.ok && i + S < q.count) issue(t + S * q.step, s);
+    at_row.next();
   }
+  if (leader) at_row.drain();
 }
 
-template <typename T, int S, bool HASY, bool POST, bool FULL, bool PRE>
+// Stages of the ring: as many as leave room for two CTAs per SM, 2 to 4.
+template <typename T, bool HASY, bool POST, bool FULL, bool PRE>
 int run_fwd(const NormFwd& p0, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
+  constexpr int row = kCols * (int)sizeof(T) * (1 + HASY + FULL);
+  constexpr int fit = kNormSmem / (row * kNormThreads * kFwdCtas), S = fit > 4 ? 4 : fit;
   NormFwd p = p0;
-  const NormPlan q = norm_plan(p.T, p.d, S * 16 * planes<T>() * (1 + HASY + FULL), kFwdCtas);
+  const NormPlan q = norm_plan(p.T, p.d, S * row, kFwdCtas);
   p.C = q.C;
   p.nt = q.nt;
   return launch_norm(block_norm_fwd<T, S, HASY, POST, FULL, PRE>, configured, p, q, st);
 }
 
-template <typename T, int S>
+template <typename T>
 int fwd_of(const NormFwd& p, cudaStream_t st) {
   const bool post = p.w_post, full = p.gate_full, pre = p.w_pre;
-  if (!p.y) return run_fwd<T, S, false, false, false, true>(p, st);
+  if (!p.y) return run_fwd<T, false, false, false, true>(p, st);
   if (post)
-    return full ? (pre ? run_fwd<T, S, true, true, true, true>(p, st)
-                       : run_fwd<T, S, true, true, true, false>(p, st))
-                : (pre ? run_fwd<T, S, true, true, false, true>(p, st)
-                       : run_fwd<T, S, true, true, false, false>(p, st));
-  return full ? (pre ? run_fwd<T, S, true, false, true, true>(p, st)
-                     : run_fwd<T, S, true, false, true, false>(p, st))
-              : (pre ? run_fwd<T, S, true, false, false, true>(p, st)
-                     : run_fwd<T, S, true, false, false, false>(p, st));
+    return full ? (pre ? run_fwd<T, true, true, true, true>(p, st)
+                       : run_fwd<T, true, true, true, false>(p, st))
+                : (pre ? run_fwd<T, true, true, false, true>(p, st)
+                       : run_fwd<T, true, true, false, false>(p, st));
+  return full ? (pre ? run_fwd<T, true, false, true, true>(p, st)
+                     : run_fwd<T, true, false, true, false>(p, st))
+              : (pre ? run_fwd<T, true, false, false, true>(p, st)
+                     : run_fwd<T, true, false, false, false>(p, st));
 }
 
 }  // namespace
@@ -177,8 +189,9 @@ extern "C" int moe_block_norm_fwd(const moe_block_norm* norm, int32_t dtype, con
   p.inv_d = 1.0f / (float)b.d;
   p.x_out = x_out;
   p.u = u;
+  p.status = status_word();
   cudaStream_t st = as_stream(stream);
-  if (dtype == MOE_F32) return fwd_of<float, 2>(p, st);
-  if (dtype == MOE_BF16) return fwd_of<__nv_bfloat16, 4>(p, st);
-  return fwd_of<__half, 4>(p, st);
+  if (dtype == MOE_F32) return fwd_of<float>(p, st);
+  if (dtype == MOE_BF16) return fwd_of<__nv_bfloat16>(p, st);
+  return fwd_of<__half>(p, st);
 }

@@ -1,18 +1,20 @@
 // Pieces of the block-norm kernels (norm.cu, norm_bwd.cu).
 //
 // A team of nt threads (a multiple of 32, at most 256) takes a row, 16 columns a
-// thread in two chunks of 8, so that the fixed work of a row (its sums'
-// shuffles, the barriers, the addresses) is spread over many columns; teams
-// walk the rows with a stride.  Each thread copies its own columns of the next
-// rows into shared memory with cp.async, S - 1 rows ahead: the copies need no
-// barrier, and nothing but the running sums and the gains stays in registers.
-// Columns past the row's end are filled with zeros, so only the stores ask for
-// them.  Arithmetic is on pairs (one instruction for two fp32 operations).
-// Rows above 4096 columns go to a cluster of two or four CTAs that exchange
-// their sums through distributed shared memory.
+// thread, so that the fixed work of a row (its sums' shuffles, the barriers, the
+// addresses) is spread over many columns; teams walk the rows with a stride.
+// One thread of a team starts bulk copies of the next rows into a ring in
+// shared memory, so that the loads in flight cost no registers and no
+// instructions of the other threads.  (Copies by every thread, cp.async, reached
+// the same bandwidth alone, but not next to the row's arithmetic: 136 us against
+// 106 for the gradients of 8192 x 4096 bf16 with fp32 stream gradients.)
+// Arithmetic is on pairs (one instruction for two fp32 operations).  Rows
+// above 4096 columns go to a cluster of two or four CTAs that exchange their sums
+// through distributed shared memory.
 #pragma once
 
 #include "common.cuh"
+#include "tc_primitives.cuh"
 
 namespace moe {
 
@@ -76,43 +78,24 @@ __device__ __forceinline__ uint32_t narrow<__half>(Pair p) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// ------------------------------------------------------- the threads' FIFO
-// A chunk is 8 columns: 16 bytes of a 16-bit type, two times 16 of fp32.  A
-// thread has two chunks of every array, and per stage of the FIFO a slot of 16
-// bytes in each plane of blockDim.x slots.
-template <typename T>
-constexpr int planes() { return 2 * (sizeof(T) == 4 ? 2 : 1); }  // of an array
+// ------------------------------------------------------------ the rows' ring
+// A thread's columns are chunks of W, nt W apart: W = 8 where every array has
+// 16-bit elements (16 bytes a thread), 4 where one has fp32, so that the
+// threads' reads of either width are of consecutive bytes.
+constexpr int kCols = 16;  // columns a thread
+template <typename T, typename G>
+constexpr int chunk_width() { return sizeof(T) == 2 && sizeof(G) == 2 ? 8 : 4; }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// 16 bytes, of which `size` (16 or 0) are read and the others are zeros.
-__device__ __forceinline__ void cp16(uint32_t smem, const void* g, uint32_t size) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(g), "r"(size)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 
-// What a thread is: its row team, its two chunks of columns.
+// What a thread is: its row team and its columns.
 struct Place {
-  int team, lane_t;     // team of this CTA, thread in the team
-  int c[2];             // first column of each chunk; 0 where there is none
-  bool on[2];           // whether the columns exist
-  uint32_t size[2];     // 16 or 0 (cp16)
-  int first, step;      // rows
-  int count;            // rows that this team takes
+  int team, lane_t;        // team of this CTA, thread in the team
+  int begin, cols;         // the columns of this CTA: first one, how many
+  uint32_t first, step;    // rows
+  int count;               // rows that this team takes
 };
 
 __device__ __forceinline__ Place place_of(int nt, int C, int d, int T) {
@@ -120,92 +103,133 @@ __device__ __forceinline__ Place place_of(int nt, int C, int d, int T) {
   q.team = threadIdx.x / nt;
   q.lane_t = threadIdx.x - q.team * nt;
   const int teams = blockDim.x / nt, rank = blockIdx.x % C;
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    q.c[v] = ((rank * 2 + v) * nt + q.lane_t) * 8;
-    q.on[v] = q.c[v] < d;
-    q.size[v] = q.on[v] ? 16 : 0;
-    if (!q.on[v]) q.c[v] = 0;
-  }
+  q.begin = rank * nt * kCols;
+  q.cols = min(nt * kCols, d - q.begin);
+  if (q.cols < 0) q.cols = 0;
   q.first = (blockIdx.x / C) * teams + q.team;
   q.step = (gridDim.x / C) * teams;
-  q.count = q.first < T ? (T - q.first - 1) / q.step + 1 : 0;
+  q.count = q.first < (uint32_t)T ? (T - q.first - 1) / q.step + 1 : 0;
   return q;
 }
 
-// One array's rows as a thread sees them: the copies walk with their own row.
-template <typename T>
-struct Stream {
-  const T* next;        // the row of the next copy
-  uint32_t at;          // its first plane in a stage
-  __device__ __forceinline__ void start(const void* p, const Place& q, int d, uint32_t plane) {
-    next = static_cast<const T*>(p) + (size_t)q.first * d;
-    at = plane;
-  }
-  // the next row into a stage (its shared address), then one step on
-  __device__ __forceinline__ void copy(const Place& q, uint32_t stage, uint32_t step, size_t skip) {
+// A chunk of W columns from shared memory.
+template <int W, typename T>
+__device__ __forceinline__ void get(uint32_t a, Pair* o) {
+  static_assert(W * sizeof(T) == 16 || W * sizeof(T) == 8, "16 or 8 bytes a thread");
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(o[0]), "=l"(o[1]) : "r"(a) : "memory");
+  } else if constexpr (W == 8) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a)
+                 : "memory");
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint32_t a = stage + (at + v * planes<T>() / 2) * step;
-      const char* src = reinterpret_cast<const char*>(next + q.c[v]);
-      cp16(a, src, q.size[v]);
-      if (sizeof(T) == 4) cp16(a + step, src + 16, q.size[v]);
-    }
-    next += skip;
+    for (int i = 0; i < 4; ++i) o[i] = widen<T>(w[i]);
+  } else {
+    uint32_t w[2];
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+    o[0] = widen<T>(w[0]);
+    o[1] = widen<T>(w[1]);
   }
-  // chunk v of a stage
-  __device__ __forceinline__ void get(int v, uint32_t stage, uint32_t step, Pair* o) const {
-    const uint32_t a = stage + (at + v * planes<T>() / 2) * step;
-    const uint4 x = lds16(a);
-    if constexpr (sizeof(T) == 4) {
-      const uint4 y = lds16(a + step);
-      o[0] = pair(__uint_as_float(x.x), __uint_as_float(x.y));
-      o[1] = pair(__uint_as_float(x.z), __uint_as_float(x.w));
-      o[2] = pair(__uint_as_float(y.x), __uint_as_float(y.y));
-      o[3] = pair(__uint_as_float(y.z), __uint_as_float(y.w));
-    } else {
-      o[0] = widen<T>(x.x);
-      o[1] = widen<T>(x.y);
-      o[2] = widen<T>(x.z);
-      o[3] = widen<T>(x.w);
-    }
-  }
-};
+}
 
 // Rounds a chunk to T and stores it; v holds the rounded values after it.
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* o, bool on, Pair* v) {
+template <int W, typename T>
+__device__ __forceinline__ void put(T* o, bool on, Pair* v) {
   if constexpr (sizeof(T) == 4) {
-    const float2 a = parts(v[0]), b = parts(v[1]), c = parts(v[2]), d = parts(v[3]);
-    if (on) {
-      reinterpret_cast<float4*>(o)[0] = make_float4(a.x, a.y, b.x, b.y);
-      reinterpret_cast<float4*>(o)[1] = make_float4(c.x, c.y, d.x, d.y);
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const float2 a = parts(v[2 * i]), b = parts(v[2 * i + 1]);
+      if (on) reinterpret_cast<float4*>(o)[i] = make_float4(a.x, a.y, b.x, b.y);
     }
   } else {
-    uint32_t w[4];
+    uint32_t w[W / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W / 2; ++i) {
       w[i] = narrow<T>(v[i]);
       v[i] = widen<T>(w[i]);
     }
-    if (on) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (W == 8) {
+      if (on) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      if (on) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    }
   }
 }
 
 // The products of the gains that are given (NULL: 1), times f.
-__device__ __forceinline__ void gains(const Place& q, const float* a, const float* b, float f,
-                                      Pair* o) {
+template <int W>
+__device__ __forceinline__ void gains(const Place& q, int nt, const float* a, const float* b,
+                                      float f, Pair* o) {
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    float w[8], z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = z[i] = 1.0f;
-    if (a) load8(a + q.c[v], w);
-    if (b) load8(b + q.c[v], z);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[4 * v + i] = pair(w[2 * i] * z[2 * i] * f, w[2 * i + 1] * z[2 * i + 1] * f);
+  for (int i = 0; i < kCols / 2; ++i) {
+    const int c = ((2 * i / W) * nt + q.lane_t) * W + 2 * i % W;
+    float2 w = make_float2(1.0f, 1.0f), z = w;
+    if (a && c < q.cols) w = *reinterpret_cast<const float2*>(a + q.begin + c);
+    if (b && c < q.cols) z = *reinterpret_cast<const float2*>(b + q.begin + c);
+    o[i] = pair(w.x * z.x * f, w.y * z.y * f);
   }
+}
+
+// Each team has a ring of S stages of its rows' arrays, filled by bulk copies
+// that its first thread starts; a stage's barrier completes when they landed.
+// Columns that the row does not have stay the zeros they are set to here.
+constexpr long long kRowWait = 4000000000LL;  // cycles (~2 s)
+constexpr int kMaxTeams = kNormThreads / 32;
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// A team's place in its ring.  A wait that runs out records an error once; the
+// team then goes on without waiting and without new copies (every thread still
+// reaches every barrier), and its first thread waits once more, again with a
+// limit, for the copies that may be in flight before it leaves.
+struct Ring {
+  uint32_t bar;       // the stages' barriers
+  int stages, s;      // s: the current stage
+  uint32_t phase;
+  bool ok;
+  int failed_s;
+  uint32_t failed_phase;
+  __device__ __forceinline__ void wait(int* status) {
+    if (ok && !tc::mbar_wait(bar + 8 * s, phase, nullptr, kRowWait)) {
+      record_error(status, MOE_ERR_TIMEOUT);
+      ok = false;
+      failed_s = s;
+      failed_phase = phase;
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++s == stages) s = 0, phase ^= 1u;
+  }
+  __device__ __forceinline__ void drain() {
+    if (ok) return;
+    for (int k = 0; k < stages; ++k) {
+      tc::mbar_wait(bar + 8 * failed_s, failed_phase, nullptr, kRowWait / 8);
+      if (++failed_s == stages) failed_s = 0, failed_phase ^= 1u;
+    }
+  }
+};
+
+// Zeros in columns [cols, nt kCols) of an array's slot of element size `size`
+// (the row's bytes are a multiple of 16), by the team.
+__device__ __forceinline__ void zero_tail(const Place& q, int nt, uint32_t slot, int size) {
+  for (int b = q.cols * size + q.lane_t * 16; b < nt * kCols * size; b += nt * 16)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(slot + b), "r"(0) : "memory");
+}
+
+__device__ __forceinline__ void team_sync(int team, int nt) {
+  if (nt == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(nt) : "memory");
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -285,7 +309,7 @@ struct NormPlan {
   size_t smem;
 };
 
-// bytes: of the FIFO per thread.  ctas: CTAs of 256 threads per SM.  Few rows
+// bytes: of the ring per thread.  ctas: CTAs of 256 threads per SM.  Few rows
 // are spread over the SMs before a CTA gets a second team.
 inline NormPlan norm_plan(int T, int d, int bytes, int ctas) {
   NormPlan q;

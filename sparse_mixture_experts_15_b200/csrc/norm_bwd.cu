@@ -8,11 +8,15 @@
 //   dw_post = out_scale gate_ch Q         dgate_ch = out_scale w_post Q
 //   dgate_tok = sum yh k dx'              dgate_full = yh k dx'
 // so two sums over the tokens carry all three gains' gradients.  The norms'
-// factors are formed again from x' and y, which the row needs anyway.
+// factors are formed again from x' and y, which the row needs anyway.  D comes
+// from sums of the inputs as well,
+//   sum yh k g dx' = r2 (sum y k g dx_out + r1 (sum y k g w_pre du
+//                    - r1^2 B / d sum y k g x')),
+// so a row needs one round of sums: one pass over its arrays forms all six, a
+// second one the outputs.
 //
-// Bound by the rows' bytes.  A row's arrays are read from the FIFO again for
-// each of the passes that need them, which costs less than the registers to
-// keep them.  The sums over the tokens stay in registers for all rows of a
+// Bound by the rows' bytes.  The second pass reads the row's arrays from
+// shared memory again, which costs less than the registers to keep them.  The sums over the tokens stay in registers for all rows of a
 // team; the teams' and then the CTAs' parts are added in order.
 #include "norm.cuh"
 
@@ -31,7 +35,67 @@ struct NormBwd {
   void *dx, *dy, *dgate_full;
   float* dgate_tok;
   float *part_pre, *part_q;  // [parts][d], nullable
+  int* status;
 };
+
+// Six sums over the threads of a row at once.  In a warp a lane hands on half of
+// its values at each of three steps, so that lane 4 i ends with value i's sum
+// after 9 shuffles instead of 30; the team's warps and then the cluster's CTAs
+// are added from shared memory by lanes that each take one value.  Two buffers
+// taken in turn: a thread writes a buffer again only after a barrier that every
+// reader of its last contents has reached.
+struct RowSumMem {
+  float warp_part[2][kNormThreads / 32][8];
+  float rank_part[2][4][8];
+};
+struct RowSum6 {
+  RowSumMem* m;
+  int team, nt, warps, C;  // warps: of this team
+  int turn;
+};
+__device__ __forceinline__ void row_sums(RowSum6& r, float* v) {
+  const int lane = threadIdx.x & 31;
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+  float h[4], a, c;
+  h[0] = (b4 ? v[4] : v[0]) + __shfl_xor_sync(0xffffffffu, b4 ? v[0] : v[4], 16);
+  h[1] = (b4 ? v[5] : v[1]) + __shfl_xor_sync(0xffffffffu, b4 ? v[1] : v[5], 16);
+  h[2] = (b4 ? 0.0f : v[2]) + __shfl_xor_sync(0xffffffffu, b4 ? v[2] : 0.0f, 16);
+  h[3] = (b4 ? 0.0f : v[3]) + __shfl_xor_sync(0xffffffffu, b4 ? v[3] : 0.0f, 16);
+  a = (b3 ? h[2] : h[0]) + __shfl_xor_sync(0xffffffffu, b3 ? h[0] : h[2], 8);
+  c = (b3 ? h[3] : h[1]) + __shfl_xor_sync(0xffffffffu, b3 ? h[1] : h[3], 8);
+  a = (b2 ? c : a) + __shfl_xor_sync(0xffffffffu, b2 ? a : c, 4);
+  a += __shfl_xor_sync(0xffffffffu, a, 2);
+  a += __shfl_xor_sync(0xffffffffu, a, 1);  // the sum of value lane / 4
+  int from = 4;                             // lanes between the values
+  const int b = r.turn;
+  if (r.warps > 1) {
+    if ((lane & 3) == 0) r.m->warp_part[b][threadIdx.x >> 5][lane >> 2] = a;
+    asm volatile("bar.sync %0, %1;" ::"r"(r.team + 1), "r"(r.nt) : "memory");
+    const float* p = &r.m->warp_part[b][r.team * r.warps][lane & 7];
+    const int w = lane >> 3;
+    a = (w < r.warps ? p[8 * w] : 0.0f) + (w + 4 < r.warps ? p[8 * (w + 4)] : 0.0f);
+    a += __shfl_xor_sync(0xffffffffu, a, 8);
+    a += __shfl_xor_sync(0xffffffffu, a, 16);
+    from = 1;
+  }
+  if (r.C > 1) {  // warps > 1: rows this wide fill their teams
+    const int rank = blockIdx.x % r.C;
+    if (threadIdx.x < 8)
+      for (int to = 0; to < r.C; ++to) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(smem_addr(&r.m->rank_part[b][rank][lane])), "r"(to));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(a) : "memory");
+      }
+    cluster_barrier();
+    a = r.m->rank_part[b][0][lane & 7];
+    for (int k = 1; k < r.C; ++k) a += r.m->rank_part[b][k][lane & 7];
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, a, from * i);
+  r.turn = b ^ 1;
+}
 
 enum RowGate { ROW_ONE = 0, ROW_TOKEN = 1, ROW_FULL = 2 };
 
@@ -39,178 +103,189 @@ enum RowGate { ROW_ONE = 0, ROW_TOKEN = 1, ROW_FULL = 2 };
 template <typename T, typename G, int S, bool PRE, bool HASY, bool POST, int GATE>
 __global__ void __launch_bounds__(kNormThreads, kBwdCtas)
     block_norm_bwd(const __grid_constant__ NormBwd p) {
-  extern __shared__ __align__(16) char fifo_mem[];
-  __shared__ SumBuffers sum_mem;
+  extern __shared__ __align__(128) char ring_mem[];
+  __shared__ RowSumMem sum_mem;
+  __shared__ uint64_t full_bar[kMaxTeams][S];
+  constexpr bool FULL = GATE == ROW_FULL, TOKEN = GATE == ROW_TOKEN;
+  constexpr bool SUMS = PRE || POST || TOKEN;
+  constexpr int W = chunk_width<T, G>(), NV = kCols / W, ET = sizeof(T), EG = sizeof(G), H = W / 2;
+  constexpr int NT = PRE + HASY + FULL, NG = PRE + 1;  // arrays of T, of G
+  const int nt = p.nt;
+  const Place q = place_of(nt, p.C, p.d, p.T);
+  RowSum6 sums{&sum_mem, q.team, nt, nt / 32, p.C, 0};
+  // a stage: x', y, the full gate, then du, dx_out
+  const uint32_t st_t = nt * kCols * ET, st_g = nt * kCols * EG;  // bytes of an array in a stage
+  const uint32_t stage = NT * st_t + NG * st_g;
+  const uint32_t oy = PRE * st_t, og = oy + HASY * st_t, ou = NT * st_t, od = ou + PRE * st_g;
+  const uint32_t ring = smem_addr(ring_mem) + q.team * S * stage;
+  const uint32_t bar = smem_addr(full_bar[q.team]);
+  const bool leader = q.lane_t == 0, has_d = p.dx_out != nullptr;
+  if (leader) {
+    for (int s = 0; s < S; ++s) tc::mbar_init(bar + 8 * s, 1);
+    tc::fence_barrier_init();
+  }
+  for (int s = 0; s < S; ++s) {
+    for (int k = 0; k < NT; ++k) zero_tail(q, nt, ring + s * stage + k * st_t, ET);
+    for (int k = 0; k < NG; ++k) zero_tail(q, nt, ring + s * stage + ou + k * st_g, EG);
+  }
+  team_sync(q.team, nt);
+  if (p.C > 1) cluster_barrier();  // every CTA of the cluster runs before its memory is written
   pdl_wait();
   pdl_allow_next();
-  const Place q = place_of(p.nt, p.C, p.d, p.T);
-  RowSum sums{&sum_mem, q.team, p.nt, p.nt / 32, p.C, 0};
-  if (p.C > 1) cluster_barrier();  // every CTA of the cluster runs before its memory is written
-  constexpr bool FULL = GATE == ROW_FULL, TOKEN = GATE == ROW_TOKEN;
-  constexpr int P = planes<T>(), PG = planes<G>();
-  constexpr int ay = P * PRE, ag = ay + P * HASY, au = ag + P * FULL, ad = au + PG * PRE;
-  const bool has_d = p.dx_out != nullptr;
-  const uint32_t step = blockDim.x * 16, stage = (ad + PG) * step;
-  const uint32_t base = smem_addr(fifo_mem + threadIdx.x * 16);
-  const size_t skip = (size_t)q.step * p.d;
-  Stream<T> sx, sy, sg;
-  Stream<G> su, sd;
-  if (PRE) sx.start(p.x_out, q, p.d, 0);
-  if (HASY) sy.start(p.y, q, p.d, ay);
-  if (FULL) sg.start(p.gate_full, q, p.d, ag);
-  if (PRE) su.start(p.du, q, p.d, au);
-  sd.start(p.dx_out, q, p.d, ad);
-  int uncopied = q.count;
-  auto issue = [&](uint32_t at) {
-    if (uncopied > 0) {
-      if (PRE) sx.copy(q, at, step, skip);
-      if (HASY) sy.copy(q, at, step, skip);
-      if (FULL) sg.copy(q, at, step, skip);
-      if (PRE) su.copy(q, at, step, skip);
-      if (has_d) sd.copy(q, at, step, skip);
-      --uncopied;
-    }
-    cp_commit();
+  auto issue = [&](uint32_t row, int s) {  // by the leader
+    const size_t e = (size_t)row * (uint32_t)p.d + q.begin;
+    const uint32_t at = ring + s * stage, bt = q.cols * ET, bg = q.cols * EG, b = bar + 8 * s;
+    tc::mbar_arrive_expect_tx(b, NT * bt + (PRE + has_d) * bg);
+    if (q.cols == 0) return;
+    if (PRE) bulk_copy(at, static_cast<const T*>(p.x_out) + e, bt, b);
+    if (HASY) bulk_copy(at + oy, static_cast<const T*>(p.y) + e, bt, b);
+    if (FULL) bulk_copy(at + og, static_cast<const T*>(p.gate_full) + e, bt, b);
+    if (PRE) bulk_copy(at + ou, static_cast<const G*>(p.du) + e, bg, b);
+    if (has_d) bulk_copy(at + od, static_cast<const G*>(p.dx_out) + e, bg, b);
   };
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(base + s * stage);
+  if (leader)
+    for (int s = 0; s < S && s < q.count; ++s) issue(q.first + s * q.step, s);
   Pair coef[8], wpre[8], a_pre[8], a_q[8];
-  gains(q, p.w_post, p.gate_ch, p.beta, coef);
-  if (PRE) gains(q, p.w_pre, nullptr, 1.0f, wpre);
+  gains<W>(q, nt, p.w_post, p.gate_ch, p.beta, coef);
+  if (PRE) gains<W>(q, nt, p.w_pre, nullptr, 1.0f, wpre);
 #pragma unroll
   for (int i = 0; i < 8; ++i) a_pre[i] = a_q[i] = 0;
   const float af = p.branch ? p.alpha : 1.0f;
   const Pair alpha = pair(af, af);
-  G* dx = static_cast<G*>(p.dx) + (size_t)q.first * p.d;
-  T* dy = static_cast<T*>(p.dy) + (size_t)q.first * p.d;
-  T* dg = static_cast<T*>(p.dgate_full) + (size_t)q.first * p.d;
-  uint32_t at = base, last = base + (S - 1) * stage;  // this row's stage, the one before it
+  const uint32_t mt = q.lane_t * W * ET, mg = q.lane_t * W * EG;  // this thread's first chunk
+  const uint32_t nx = nt * W * ET, ng = nt * W * EG;              // from a chunk to the next
   uint32_t t = q.first;
-  for (int left = q.count; left > 0; --left, t += q.step) {
-    issue(last);
+  Ring at_row{bar, S, 0, 0, true, 0, 0};
+  for (int row = 0; row < q.count; ++row, t += q.step) {
     const float gt = TOKEN ? p.gate_tok[t] : 1.0f;
-    cp_wait<S - 1>();
-    float s3[3] = {0.0f, 0.0f, 0.0f};
-    {
-      Pair sa = 0, sb = 0, sc = 0;
+    at_row.wait(p.status);
+    const int s = at_row.s;
+    const uint32_t ax = ring + s * stage + mt, ay = ax + oy, ag = ax + og;
+    const uint32_t au = ring + s * stage + ou + mg, ad = ring + s * stage + od + mg;
+    // pass 1: the sums over the row
+    float r1 = 1.0f, r2 = 1.0f, m1 = 0.0f, D = 0.0f;  // D without a token's gate
+    if (SUMS) {
+      Pair sums6[6] = {0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        Pair x[4], u[4];
+      for (int v = 0; v < NV; ++v) {
+        Pair x[H], u[H], y[H], d[H];
         if (PRE) {
-          sx.get(v, at, step, x);
-          su.get(v, at, step, u);
+          get<W, T>(ax + v * nx, x);
+          get<W, G>(au + v * ng, u);
+        }
+        if (HASY) get<W, T>(ay + v * nx, y);
+        if (HASY && (POST || TOKEN) && has_d) get<W, G>(ad + v * ng, d);
+        if (POST)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sa = fma2(x[i], x[i], sa);
-            sb = fma2(mul2(x[i], wpre[4 * v + i]), u[i], sb);
+          for (int i = 0; i < H; ++i) sums6[2] = fma2(y[i], y[i], sums6[2]);
+        if (FULL && POST) {
+          Pair g[H];
+          get<W, T>(ag + v * nx, g);
+#pragma unroll
+          for (int i = 0; i < H; ++i) y[i] = mul2(y[i], g[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const int k = H * v + i;
+          Pair w = 0;
+          if (PRE) {
+            w = mul2(u[i], wpre[k]);
+            sums6[0] = fma2(x[i], x[i], sums6[0]);
+            sums6[1] = fma2(x[i], w, sums6[1]);
+          }
+          if (POST || TOKEN) {
+            const Pair z = mul2(y[i], coef[k]);
+            if (has_d) sums6[3] = fma2(z, d[i], sums6[3]);
+            if (PRE) {
+              sums6[4] = fma2(z, w, sums6[4]);
+              sums6[5] = fma2(z, x[i], sums6[5]);
+            }
           }
         }
-        if (POST) {
-          sy.get(v, at, step, x);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc = fma2(x[i], x[i], sc);
-        }
       }
-      s3[0] = sum2(sc), s3[1] = sum2(sa), s3[2] = sum2(sb);
-    }
-    if (PRE) row_sum<3>(sums, s3);
-    else if (POST) row_sum<1>(sums, s3);
-    Pair dv[8];
-    if (has_d) {
+      float s6[6];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) sd.get(v, at, step, dv + 4 * v);
+      for (int i = 0; i < 6; ++i) s6[i] = sum2(sums6[i]);
+      row_sums(sums, s6);
+      if (PRE) {
+        r1 = rsqrtf(fmaf(s6[0], p.inv_d, p.eps));
+        m1 = -s6[1] * p.inv_d * r1 * r1;
+      }
+      if (POST) r2 = rsqrtf(fmaf(s6[2], p.inv_d, p.eps));
+      D = fmaf(r1, fmaf(m1, s6[5], s6[4]), s6[3]) * r2;
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dv[i] = 0;
+      team_sync(q.team, nt);
     }
-    if (PRE) {
-      const float r1 = rsqrtf(fmaf(s3[1], p.inv_d, p.eps)), m = -s3[2] * p.inv_d * r1 * r1;
-      const Pair rr = pair(r1, r1), mm = pair(m, m);
+    // every thread of the team is past the row before this one: its stage is free
+    if (nt == 32) __syncwarp();
+    if (leader && at_row.ok && row > 0 && row - 1 + S < q.count)
+      issue(t + (S - 1) * q.step, s == 0 ? S - 1 : s - 1);
+    if (TOKEN && q.begin + q.lane_t == 0) p.dgate_tok[t] = D;
+    // pass 2: the outputs
+    const float my = POST ? -D * gt * p.inv_d * r2 * r2 : 0.0f;
+    const Pair rr1 = pair(r1, r1), mm1 = pair(m1, m1), rr2 = pair(r2, r2), mm2 = pair(my, my);
+    const size_t e = (size_t)t * (uint32_t)p.d + q.begin + q.lane_t * W;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        Pair x[4], u[4];
-        sx.get(v, at, step, x);
-        su.get(v, at, step, u);
+    for (int v = 0; v < NV; ++v) {
+      const bool on = (v * nt + q.lane_t) * W < q.cols;
+      const size_t ev = e + v * nt * W;
+      Pair dv[H], y[H], z[H];
+      if (has_d) {
+        get<W, G>(ad + v * ng, dv);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 4 * v + i;
-          dv[k] = fma2(fma2(x[i], mm, mul2(wpre[k], u[i])), rr, dv[k]);
-          a_pre[k] = fma2(u[i], mul2(x[i], rr), a_pre[k]);
+        for (int i = 0; i < H; ++i) dv[i] = 0;
+      }
+      if (PRE) {
+        Pair x[H], u[H];
+        get<W, T>(ax + v * nx, x);
+        get<W, G>(au + v * ng, u);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const int k = H * v + i;
+          dv[i] = fma2(fma2(x[i], mm1, mul2(wpre[k], u[i])), rr1, dv[i]);
+          a_pre[k] = fma2(u[i], mul2(x[i], rr1), a_pre[k]);
         }
       }
-    }
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      Pair z[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = mul2(dv[4 * v + i], alpha);
-      store_chunk<G>(dx + q.c[v], q.on[v], z);
-    }
-    dx += skip;
-    if (p.branch) {
-      const float r2 = POST ? rsqrtf(fmaf(s3[0], p.inv_d, p.eps)) : 1.0f;
-      const Pair rr = pair(r2, r2);
-      Pair sum = 0;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        Pair y[4], g[4];
-        if (HASY) {
-          sy.get(v, at, step, y);
-          if (POST)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], rr);
-        }
+      for (int i = 0; i < H; ++i) z[i] = mul2(dv[i], alpha);
+      put<W>(static_cast<G*>(p.dx) + ev, on, z);
+      if (!p.branch) continue;
+      if (HASY) {
+        get<W, T>(ay + v * nx, y);
         if (FULL) {
-          sg.get(v, at, step, g);
-          Pair z[4];
+          Pair g[H];
+          get<W, T>(ag + v * nx, g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            z[i] = mul2(mul2(coef[4 * v + i], dv[4 * v + i]), y[i]);
-            dv[4 * v + i] = mul2(dv[4 * v + i], g[i]);
+          for (int i = 0; i < H; ++i) {
+            z[i] = mul2(mul2(coef[H * v + i], dv[i]), mul2(y[i], rr2));
+            dv[i] = mul2(dv[i], g[i]);
           }
-          store_chunk<T>(dg + q.c[v], q.on[v], z);
-        }
-        // dv becomes k g dx', but for a token's gate, which comes in below
+          put<W>(static_cast<T*>(p.dgate_full) + ev, on, z);
+        } else if (TOKEN) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 4 * v + i;
-          if (HASY) a_q[k] = fma2(TOKEN ? mul2(dv[k], pair(gt, gt)) : dv[k], y[i], a_q[k]);
-          dv[k] = mul2(dv[k], coef[k]);
-          if (HASY) sum = fma2(dv[k], y[i], sum);
+          for (int i = 0; i < H; ++i) dv[i] = mul2(dv[i], pair(gt, gt));
         }
-      }
-      dg += skip;
-      float m = 0.0f;
-      if (POST || TOKEN) {
-        float s1[1] = {sum2(sum)};
-        row_sum<1>(sums, s1);
-        if (TOKEN && q.lane_t == 0 && (p.C == 1 || blockIdx.x % p.C == 0)) p.dgate_tok[t] = s1[0];
-        m = -s1[0] * gt * p.inv_d * r2 * r2;
-      }
-      const float ro = r2 * gt;
-      const Pair mm = pair(m, m), rg = pair(ro, ro);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        Pair y[4];
-        if (POST) sy.get(v, at, step, y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 4 * v + i;
-          if (POST || TOKEN) dv[k] = mul2(dv[k], rg);
-          if (POST) dv[k] = fma2(y[i], mm, dv[k]);
+        for (int i = 0; i < H; ++i) {
+          const int k = H * v + i;
+          a_q[k] = fma2(dv[i], POST ? mul2(y[i], rr2) : y[i], a_q[k]);
+          z[i] = mul2(dv[i], coef[k]);
+          if (POST) z[i] = fma2(z[i], rr2, mul2(y[i], mm2));
         }
-        store_chunk<T>(dy + q.c[v], q.on[v], dv + 4 * v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < H; ++i) z[i] = mul2(dv[i], coef[H * v + i]);
       }
-      dy += skip;
+      put<W>(static_cast<T*>(p.dy) + ev, on, z);
     }
-    last = at;
-    at = at == base + (S - 1) * stage ? base : at + stage;
+    at_row.next();
   }
-  // The CTA's teams add their columns' sums in team order, through the FIFO's
-  // memory once every copy into it has landed.
-  cp_wait<0>();
-  const int teams = blockDim.x / p.nt;
-  Pair* mem = reinterpret_cast<Pair*>(fifo_mem);
+  if (leader) at_row.drain();
+  // The CTA's teams add their columns' sums in team order, through the ring's
+  // memory: every copy into it has been waited for.
+  const int teams = blockDim.x / nt;
+  Pair* mem = reinterpret_cast<Pair*>(ring_mem);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float* out = k == 0 ? p.part_pre : p.part_q;
@@ -225,55 +300,59 @@ __global__ void __launch_bounds__(kNormThreads, kBwdCtas)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           for (int m = 1; m < teams; ++m)
-            a[i] = fma2(mem[i * blockDim.x + m * p.nt + q.lane_t], pair(1.0f, 1.0f), a[i]);
+            a[i] = fma2(mem[i * blockDim.x + m * nt + q.lane_t], pair(1.0f, 1.0f), a[i]);
     }
     if (q.team == 0)
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        store_chunk<float>(out + (size_t)(blockIdx.x / p.C) * p.d + q.c[v], q.on[v], a + 4 * v);
+      for (int v = 0; v < NV; ++v)
+        put<W>(out + (size_t)(blockIdx.x / p.C) * p.d + q.begin + (v * nt + q.lane_t) * W,
+               (v * nt + q.lane_t) * W < q.cols, a + H * v);
   }
 }
 
-// The gains' gradients from the parts: 32 columns for a block, 8 runs of parts
-// summed at once and the runs then in order.
+// The gains' gradients from the parts: 32 columns for a block, 32 runs of parts
+// summed at once (the loads of a run are in flight together), then the runs by
+// a shuffle tree.
 struct NormSums {
   int parts, d;
   const float *part_pre, *part_q, *w_post, *gate_ch;
   float beta;
   float *dw_pre, *dw_post, *dgate_ch;
 };
-__global__ void __launch_bounds__(256) block_norm_sums(const __grid_constant__ NormSums p) {
+__global__ void __launch_bounds__(1024) block_norm_sums(const __grid_constant__ NormSums p) {
   pdl_wait();
   pdl_allow_next();
-  __shared__ float run[8][32];
-  const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;
+  __shared__ float run[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const float* src = blockIdx.y == 0 ? p.part_pre : p.part_q;
   if (!src) return;
   float a = 0.0f;
-  if (c < p.d) {
-    src += c;
-#pragma unroll 8
-    for (int i = r; i < p.parts; i += 8) a += src[(size_t)i * p.d];
+  if (blockIdx.x * 32 + lane < p.d) {
+    src += blockIdx.x * 32 + lane;
+#pragma unroll 10
+    for (int i = w; i < p.parts; i += 32) a += src[(size_t)i * p.d];
   }
-  run[r][lane] = a;
+  run[w][lane] = a;
   __syncthreads();
-  if (r == 0 && c < p.d) {
+  a = run[lane][w];  // column w of the block
 #pragma unroll
-    for (int i = 1; i < 8; ++i) a += run[i][lane];
-    if (blockIdx.y == 0) {
-      p.dw_pre[c] = a;
-    } else {
-      if (p.dw_post) p.dw_post[c] = p.beta * (p.gate_ch ? p.gate_ch[c] : 1.0f) * a;
-      if (p.dgate_ch) p.dgate_ch[c] = p.beta * (p.w_post ? p.w_post[c] : 1.0f) * a;
-    }
+  for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  const int c = blockIdx.x * 32 + w;
+  if (lane != 0 || c >= p.d) return;
+  if (blockIdx.y == 0) {
+    p.dw_pre[c] = a;
+  } else {
+    if (p.dw_post) p.dw_post[c] = p.beta * (p.gate_ch ? p.gate_ch[c] : 1.0f) * a;
+    if (p.dgate_ch) p.dgate_ch[c] = p.beta * (p.w_post ? p.w_post[c] : 1.0f) * a;
   }
 }
 
-// Stages of the FIFO: as many as leave room for two CTAs per SM, 2 or 3.
+// Stages of the ring: as many as leave room for two CTAs per SM, 2 or 3.
 template <typename T, typename G, bool PRE, bool HASY, bool POST, int GATE>
 int run_bwd(const NormBwd& p0, const moe_block_norm_grads& g, float* parts, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
-  constexpr int row = 16 * (planes<T>() * (PRE + HASY + (GATE == ROW_FULL)) + planes<G>() * (PRE + 1));
+  constexpr int row =
+      kCols * ((int)sizeof(T) * (PRE + HASY + (GATE == ROW_FULL)) + (int)sizeof(G) * (PRE + 1));
   constexpr int S = 3 * row * kNormThreads * kBwdCtas <= kNormSmem ? 3 : 2;
   NormBwd p = p0;
   NormPlan q = norm_plan(p.T, p.d, S * row, kBwdCtas);
@@ -296,7 +375,7 @@ int run_bwd(const NormBwd& p0, const moe_block_norm_grads& g, float* parts, cuda
       launch_norm(block_norm_bwd<T, G, S, PRE, HASY, POST, GATE>, configured, p, q, st);
   if (rc != MOE_OK || (!s.dw_pre && !q_sum)) return rc;
   MOE_PREFER_SHARED((block_norm_sums));
-  launch_pdl(block_norm_sums, dim3((p.d + 31) / 32, q_sum ? 2 : 1), dim3(256), 0, st, s);
+  launch_pdl(block_norm_sums, dim3((p.d + 31) / 32, q_sum ? 2 : 1), dim3(1024), 0, st, s);
   return launch_status();
 }
 
@@ -382,6 +461,7 @@ extern "C" int moe_block_norm_bwd(const moe_block_norm* norm, int32_t dtype, int
   p.dy = g.dy;
   p.dgate_full = b.gate == MOE_GATE_FULL ? g.dgate : nullptr;
   p.dgate_tok = b.gate == MOE_GATE_TOKEN ? static_cast<float*>(g.dgate) : nullptr;
+  p.status = status_word();
   float* parts = static_cast<float*>(ws);
   if (dtype == MOE_F32) return bwd_of<float, float>(p, g, parts, st);
   if (dtype == MOE_BF16)
