@@ -128,18 +128,26 @@ struct SelectParams {
 };
 
 // One warp per token.
+//
+// The k best of a token: with m the k-th largest of the 32 lanes' own largest
+// orders, every selected expert has an order of m at least, and few others do
+// (some 10 of 256 experts for k = 8, 23 of 896 for k = 16).  These are listed in
+// shared memory, one for a lane, and each finds its slot by counting those ahead
+// of it.  Where more than 32 qualify (ties, k near 32), the k are taken one
+// after another instead.
 template <int PER>
 __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_constant__ SelectParams p) {
   using L = Lanes<PER>;
-  extern __shared__ __align__(16) float sel_mem[];  // per warp: scores [N], then (groups) c [N]
+  extern __shared__ __align__(16) float sel_mem[];  // per warp: scores, orders [N up to 4]
+  __shared__ uint2 listed[kSelWarps][32];           // (order, expert)
   pdl_wait();
   pdl_allow_next();
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, N = p.N;
   const int64_t t = (int64_t)blockIdx.x * kSelWarps + wib;
   if (t >= p.T) return;
-  const bool groups = p.n_group > 1;
-  float* sc = sel_mem + (size_t)wib * N * (groups ? 2 : 1);
-  float* cs = sc + N;
+  const int stride = (N + 3) & ~3;
+  float* sc = sel_mem + (size_t)wib * 2 * stride;
+  uint32_t* od = reinterpret_cast<uint32_t*>(sc + stride);
   float z[PER];
   L::load(p.logits + t * N, N, lane, -INFINITY, z);
   // scores
@@ -180,16 +188,23 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
     const int j = L::expert(lane, e);
-    ord[e] = 0u;
-    if (j < N) {
-      const float c = p.bias ? z[e] + p.bias[j] : z[e];
-      sc[j] = z[e];
-      if (groups) cs[j] = c;
-      ord[e] = order_of(c);
+    ord[e] = j < N ? order_of(p.bias ? z[e] + p.bias[j] : z[e]) : 0u;
+  }
+#pragma unroll
+  for (int e = 0; e < PER; e += L::CH) {
+    const int j = L::expert(lane, e);
+    if (j >= N) continue;
+    if constexpr (L::CH == 4) {
+      *reinterpret_cast<float4*>(sc + j) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+      *reinterpret_cast<uint4*>(od + j) = make_uint4(ord[e], ord[e + 1], ord[e + 2], ord[e + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < L::CH; ++i)
+        if (j + i < N) sc[j + i] = z[e + i], od[j + i] = ord[e + i];
     }
   }
   __syncwarp();
-  if (groups) {
+  if (p.n_group > 1) {
     // sub lanes of a group read its experts in turn and keep the two best
     const int G = p.n_group, per = N / G;
     int sub = 32;
@@ -197,8 +212,9 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
     const int g = lane / sub;
     uint32_t b1 = 0u, b2 = 0u;
     if (g < G) {
+      const uint32_t* og = od + g * per;
       for (int i = lane % sub; i < per; i += sub) {
-        const uint32_t o = order_of(cs[g * per + i]);
+        const uint32_t o = og[i];
         b2 = max(b2, min(b1, o));
         b1 = max(b1, o);
       }
@@ -217,43 +233,84 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
       rank += o > mine || (o == mine && h < g);
     }
     const uint32_t kept = __ballot_sync(0xffffffffu, g < G && rank < p.top_group);
+    // j / per as a product: exact for j < 1024
+    const uint32_t inv = (1u << 20) / per + 1;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int j = L::expert(lane, e);
-      if (j < N && !((kept >> (j / per * sub)) & 1u)) ord[e] = 0u;
+      const uint32_t h = L::expert(lane, e) * inv >> 20;
+      if (h < (uint32_t)G && !((kept >> (h * sub)) & 1u)) ord[e] = 0u;
     }
   }
-  // the k best, one at a time: the largest order, then the lowest expert of it
   uint32_t best = 0u;
-  int at = 0;
 #pragma unroll
-  for (int e = 0; e < PER; ++e)
-    if (ord[e] > best) best = ord[e], at = e;
-  int mine = 0;
-  for (int s = 0; s < p.k; ++s) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int j = best == top ? L::expert(lane, at) : INT32_MAX;
-    const int w = __reduce_min_sync(0xffffffffu, j);
-    if (lane == s) mine = w;
-    if (j == w) {  // this lane's is taken
-      best = 0u;
-      int next = 0;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        if (e == at) ord[e] = 0u;
-        if (ord[e] > best) best = ord[e], next = e;
-      }
-      at = next;
-    }
+  for (int e = 0; e < PER; ++e) best = max(best, ord[e]);
+  uint32_t m = best, least = 0u;
+  for (int s = 0; s < p.k; ++s) {  // equal ones go together: that only lowers the bound
+    least = __reduce_max_sync(0xffffffffu, m);
+    if (m == least) m = 0u;
   }
-  float a = lane < p.k ? sc[mine] : 0.0f;
+  if (least == 0u) least = 1u;
+  uint32_t in = 0u;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) in |= (uint32_t)(ord[e] >= least) << e;
+  const int own = __popc(in);
+  int at = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  const int count = __shfl_sync(0xffffffffu, at, 31);
+  int slot = 32, mine = 0;  // this lane's selected expert and its slot
+  if (count <= 32) {
+    at -= own;
+    while (in) {
+      const int j = L::expert(lane, __ffs(in) - 1);
+      listed[wib][at++] = make_uint2(od[j], j);
+      in &= in - 1;
+    }
+    __syncwarp();
+    const uint2 c = lane < count ? listed[wib][lane] : make_uint2(0u, 0u);
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const uint2 o = listed[wib][i];
+      ahead += o.x > c.x || (o.x == c.x && o.y < c.y);
+    }
+    mine = c.y;
+    if (lane < count) slot = ahead;
+  } else {
+    int first = 0;  // this lane's best
+#pragma unroll
+    for (int e = PER - 1; e >= 0; --e)
+      if (ord[e] == best) first = e;
+    for (int s = 0; s < p.k; ++s) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      const int j = best == top ? L::expert(lane, first) : INT32_MAX;
+      const int w = __reduce_min_sync(0xffffffffu, j);
+      if (lane == s) mine = w;
+      if (j == w) {  // this lane's is taken
+        best = 0u;
+        int next = 0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          if (e == first) ord[e] = 0u;
+          if (ord[e] > best) best = ord[e], next = e;
+        }
+        first = next;
+      }
+    }
+    slot = lane;
+  }
+  const bool taken = slot < p.k;
+  float a = taken ? sc[mine] : 0.0f;
   if (p.renorm) {
     const float S = warp_sum(a);
     a = S == 0.0f ? 0.0f : a / S;  // nothing but zero scores: no weight
   }
-  if (lane < p.k) {
-    p.top_idx[t * p.k + lane] = mine;
-    p.top_w[t * p.k + lane] = a * p.scale;
+  if (taken) {
+    p.top_idx[t * p.k + slot] = mine;
+    p.top_w[t * p.k + slot] = a * p.scale;
   }
 }
 
@@ -424,7 +481,7 @@ int launch_select(const moe_shape& s, const moe_gating& g, const float* logits, 
                  g.group_top, g.scale, logits, bias, top_idx, top_w, scores};
   // every group kept is no limit
   if (g.top_group == g.n_group) p.n_group = 1;
-  return by_width<Select>(p, (size_t)kSelWarps * s.N * 4 * (p.n_group > 1 ? 2 : 1), st);
+  return by_width<Select>(p, (size_t)kSelWarps * ((s.N + 3) & ~3) * 8, st);
 }
 
 }  // namespace
