@@ -566,111 +566,136 @@ def moe_latent_fwd_e4m3(s: MoeShape, w_route, w_gate, w_up, w_down, gate_scale, 
 # -------------------------------- scored routing, block norms, 8-bit integers
 # These calls run on the device of their tensors, which must be one device:
 # its current stream unless one is given, whatever device is current.
-class _Call:
-    """One call's tensors: take() checks one as _need and _ptr do, and that it
-    is on the call's device (that of the first), and returns its address."""
+class _Types:
+    """torch and the element-type sets of these calls, looked up once."""
 
-    def __init__(self):
+    def __getattr__(self, name):
         import torch
-        self.torch, self.device = torch, None
+        self.torch = torch
+        self.f32, self.i32, self.i8 = (torch.float32,), (torch.int32,), (torch.int8,)
+        self.act = (torch.float32, torch.bfloat16, torch.float16)
+        self.code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        return self.__dict__[name]
 
-    def take(self, what, t, n, dtypes):
-        if t is None:
-            return None
+
+_t = _Types()
+
+
+def _addr(what, t, n, dtypes, dev):
+    """Device address of one tensor of a call on device dev, checked as _need
+    and _ptr do, and that it is on that device."""
+    if t is None:
+        return None
+    if (t.numel() < n or t.dtype not in dtypes or t.get_device() != dev
+            or not t.is_contiguous()):
         if t.numel() < n:
             raise ValueError(f"{what}: {t.numel()} elements, the call needs at least {n}")
         if t.dtype not in dtypes:
             names = " or ".join(str(x).replace("torch.", "") for x in dtypes)
             raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, "
                              f"the call needs {names}")
-        p = _ptr(t)
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{what}: on {t.device}, the call's other tensors on {self.device}")
-        return p
+        _ptr(t)
+        raise ValueError(f"{what}: on {t.device}, the call's other tensors on cuda:{dev}")
+    return t.data_ptr()
 
-    def workspace(self, nbytes, ws):
-        """(address, bytes) of a workspace of the call's device; the tensor is
-        kept until the call has been made."""
-        if nbytes == 0:
-            return None, 0
-        self.ws, n = _ws(nbytes, self.device, ws)
-        if self.ws.device != self.device:
-            raise ValueError(f"ws: on {self.ws.device}, the call's tensors on {self.device}")
-        return _ptr(self.ws), n
 
-    def run(self, where, stream, *args):
-        if self.device is None:
-            raise ValueError(f"{where}: no tensor to take the device from")
-        cuda, fn = self.torch.cuda, getattr(_lib, where)
-        if stream is None:
-            stream = cuda.current_stream(self.device).cuda_stream
-        if cuda.current_device() == self.device.index:
-            _check(fn(*args, int(stream)), where)
-        else:
-            with cuda.device(self.device):
-                _check(fn(*args, int(stream)), where)
+def _device(what, t, n, dtypes):
+    """The device of a call: that of its first tensor, checked before it."""
+    dev = t.get_device()
+    _addr(what, t, n, dtypes, dev)
+    if dev < 0:
+        _ptr(t)
+    return dev
+
+
+def _run(where, dev, stream, *args):
+    """The C call on device dev and its current stream unless one is given."""
+    if stream is None:
+        stream = _t.raw_stream(dev)
+    if _t.torch.cuda.current_device() == dev:
+        rc = getattr(_lib, where)(*args, stream)
+    else:
+        with _t.torch.cuda.device(dev):
+            rc = getattr(_lib, where)(*args, stream)
+    if rc != 0:
+        raise MoeError(rc, where)
+
+
+def _workspace(ws, dev, stream, query, *args):
+    """(address, bytes, tensor) of a workspace: the caller's, whose size the
+    library checks, or one of the queried size, which a given stream then holds
+    until its work so far is done; keep the tensor until the call is made."""
+    if ws is None:
+        cuda = _t.torch.cuda
+        with cuda.device(dev):
+            n = int(query(*args))
+        if n == 0:
+            return None, 0, None
+        ws = _t.torch.empty(max(n, 256), dtype=_t.torch.uint8, device=f"cuda:{dev}")
+        if stream is not None and int(stream) != _t.raw_stream(dev):
+            # it is from the current stream's memory, and used on another
+            ws.record_stream(cuda.ExternalStream(int(stream), device=dev))
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws: on {ws.device}, the call's tensors on cuda:{dev}")
+    return _ptr(ws), ws.numel() * ws.element_size(), ws
 
 
 def moe_route_select(s: MoeShape, g: MoeGating, logits, top_idx, top_w, bias=None, scores=None,
                      stream=None):
     """Selection and weights from the router logits (include/moe.h)."""
-    c = _Call()
-    f32, i32 = (c.torch.float32,), (c.torch.int32,)
-    TN, Tk = s.T * s.N, s.T * s.k
-    c.run("moe_route_select", stream, ctypes.byref(s), ctypes.byref(g),
-          c.take("logits", logits, TN, f32), c.take("bias", bias, s.N, f32),
-          c.take("top_idx", top_idx, Tk, i32), c.take("top_w", top_w, Tk, f32),
-          c.take("scores", scores, TN, f32))
+    T, N = s.T, s.N
+    TN, Tk, f32 = T * N, T * s.k, _t.f32
+    dev = _device("logits", logits, TN, f32)
+    _run("moe_route_select", dev, stream, ctypes.byref(s), ctypes.byref(g), logits.data_ptr(),
+         _addr("bias", bias, N, f32, dev), _addr("top_idx", top_idx, Tk, _t.i32, dev),
+         _addr("top_w", top_w, Tk, f32, dev), _addr("scores", scores, TN, f32, dev))
 
 
 def moe_route_scored(s: MoeShape, g: MoeGating, u, w_route, top_idx, top_w, bias=None,
                      scores=None, logits=None, ws=None, stream=None):
     """Router logits and the selection from them; bias is the selection's."""
-    c = _Call()
-    t = c.torch
-    f32, i32 = (t.float32,), (t.int32,)
-    TN, Tk = s.T * s.N, s.T * s.k
-    args = (c.take("u", u, s.T * s.d, (t.float32, t.bfloat16, t.float16)), _dtype_code(u),
-            c.take("w_route", w_route, s.N * s.d, f32), c.take("bias", bias, s.N, f32),
-            c.take("top_idx", top_idx, Tk, i32), c.take("top_w", top_w, Tk, f32),
-            c.take("scores", scores, TN, f32), c.take("logits", logits, TN, f32))
-    nb = 0 if logits is not None else _lib.moe_route_scored_workspace_bytes(ctypes.byref(s))
-    c.run("moe_route_scored", stream, ctypes.byref(s), ctypes.byref(g), *args,
-          *c.workspace(nb, ws))
+    TN, Tk, f32 = s.T * s.N, s.T * s.k, _t.f32
+    dev = _device("u", u, s.T * s.d, _t.act)
+    args = (u.data_ptr(), _t.code[u.dtype], _addr("w_route", w_route, s.N * s.d, f32, dev),
+            _addr("bias", bias, s.N, f32, dev), _addr("top_idx", top_idx, Tk, _t.i32, dev),
+            _addr("top_w", top_w, Tk, f32, dev), _addr("scores", scores, TN, f32, dev),
+            _addr("logits", logits, TN, f32, dev))
+    p, n, keep = (None, 0, None) if logits is not None else _workspace(
+        ws, dev, stream, _lib.moe_route_scored_workspace_bytes, ctypes.byref(s))
+    _run("moe_route_scored", dev, stream, ctypes.byref(s), ctypes.byref(g), *args, p, n)
 
 
 def moe_route_select_bwd(s: MoeShape, g: MoeGating, logits, top_idx, d_top_w, dz, d_scores=None,
                          stream=None):
     """Gradient of the weights (and scores) to the router logits."""
-    c = _Call()
-    f32 = (c.torch.float32,)
-    TN, Tk = s.T * s.N, s.T * s.k
-    c.run("moe_route_select_bwd", stream, ctypes.byref(s), ctypes.byref(g),
-          c.take("logits", logits, TN, f32), c.take("top_idx", top_idx, Tk, (c.torch.int32,)),
-          c.take("d_top_w", d_top_w, Tk, f32), c.take("d_scores", d_scores, TN, f32),
-          c.take("dz", dz, TN, f32))
+    TN, Tk, f32 = s.T * s.N, s.T * s.k, _t.f32
+    dev = _device("logits", logits, TN, f32)
+    _run("moe_route_select_bwd", dev, stream, ctypes.byref(s), ctypes.byref(g), logits.data_ptr(),
+         _addr("top_idx", top_idx, Tk, _t.i32, dev), _addr("d_top_w", d_top_w, Tk, f32, dev),
+         _addr("d_scores", d_scores, TN, f32, dev), _addr("dz", dz, TN, f32, dev))
 
 
-def _gate_args(b: MoeBlockNorm, c: _Call, what, t, dt):
-    n, types = {GATE_CHANNEL: (b.d, (c.torch.float32,)), GATE_TOKEN: (b.T, (c.torch.float32,)),
-                GATE_FULL: (b.T * b.d, dt)}.get(b.gate, (0, dt))
-    return c.take(what, t, n, types)
+def _gate(b: MoeBlockNorm, what, t, dt, dev):
+    if t is None:
+        return None
+    n, types = {GATE_CHANNEL: (b.d, _t.f32), GATE_TOKEN: (b.T, _t.f32),
+                GATE_FULL: (b.T * b.d, dt)}.get(b.gate, (0, _t.act))
+    return _addr(what, t, n, types, dev)
 
 
 def moe_block_norm_fwd(b: MoeBlockNorm, x, y=None, w_post=None, gate=None, w_pre=None, x_out=None,
                        u=None, stream=None):
     """x_out = res_scale x + out_scale gate norm(y) and u = norm(x_out)."""
-    c = _Call()
-    t = c.torch
-    n, f32 = b.T * b.d, (t.float32,)
-    px = c.take("x", x, n, (t.float32, t.bfloat16, t.float16))
+    d, f32 = b.d, _t.f32
+    n = b.T * d
+    dev = _device("x", x, n, _t.act)
     dt = (x.dtype,)
-    c.run("moe_block_norm_fwd", stream, ctypes.byref(b), _dtype_code(x), px,
-          c.take("y", y, n, dt), c.take("w_post", w_post, b.d, f32),
-          _gate_args(b, c, "gate", gate, dt), c.take("w_pre", w_pre, b.d, f32),
-          c.take("x_out", x_out, n, dt), c.take("u", u, n, dt))
+    _run("moe_block_norm_fwd", dev, stream, ctypes.byref(b), _t.code[x.dtype], x.data_ptr(),
+         _addr("y", y, n, dt, dev), _addr("w_post", w_post, d, f32, dev),
+         _gate(b, "gate", gate, dt, dev), _addr("w_pre", w_pre, d, f32, dev),
+         _addr("x_out", x_out, n, dt, dev), _addr("u", u, n, dt, dev))
 
 
 def moe_block_norm_bwd_workspace_bytes(b: MoeBlockNorm) -> int:
@@ -682,34 +707,30 @@ def moe_block_norm_bwd(b: MoeBlockNorm, dx_out, grads: dict, x_out=None, y=None,
     """Gradients of moe_block_norm_fwd: grads holds the outputs dx, dy (None
     or absent: the forward had no y), dgate, dw_post and dw_pre.  The storage
     type is that of x_out, y or dy, the gradients' type that of dx."""
-    c = _Call()
-    t = c.torch
-    n, f32, act = b.T * b.d, (t.float32,), (t.float32, t.bfloat16, t.float16)
-    dx = grads["dx"]
-    like = next((v for v in (x_out, y, grads.get("dy")) if v is not None), dx)
-    px = c.take("dx", dx, n, act)
+    d, f32 = b.d, _t.f32
+    n, dx, dy = b.T * d, grads["dx"], grads.get("dy")
+    like = x_out if x_out is not None else y if y is not None else dy if dy is not None else dx
+    dev = _device("dx", dx, n, _t.act)
     gt, dt = (dx.dtype,), (like.dtype,)
-    G = MoeBlockNormGrads(px, c.take("dy", grads.get("dy"), n, dt),
-                          _gate_args(b, c, "dgate", grads.get("dgate"), dt),
-                          c.take("dw_post", grads.get("dw_post"), b.d, f32),
-                          c.take("dw_pre", grads.get("dw_pre"), b.d, f32))
-    args = (c.take("x_out", x_out, n, dt), c.take("y", y, n, dt),
-            c.take("w_post", w_post, b.d, f32), _gate_args(b, c, "gate", gate, dt),
-            c.take("w_pre", w_pre, b.d, f32), c.take("dx_out", dx_out, n, gt),
-            c.take("du", du, n, gt))
-    c.run("moe_block_norm_bwd", stream, ctypes.byref(b), _dtype_code(like), _dtype_code(dx), *args,
-          ctypes.byref(G), *c.workspace(moe_block_norm_bwd_workspace_bytes(b), ws))
+    G = MoeBlockNormGrads(dx.data_ptr(), _addr("dy", dy, n, dt, dev),
+                          _gate(b, "dgate", grads.get("dgate"), dt, dev),
+                          _addr("dw_post", grads.get("dw_post"), d, f32, dev),
+                          _addr("dw_pre", grads.get("dw_pre"), d, f32, dev))
+    args = (_addr("x_out", x_out, n, dt, dev), _addr("y", y, n, dt, dev),
+            _addr("w_post", w_post, d, f32, dev), _gate(b, "gate", gate, dt, dev),
+            _addr("w_pre", w_pre, d, f32, dev), _addr("dx_out", dx_out, n, gt, dev),
+            _addr("du", du, n, gt, dev))
+    p, nb, keep = _workspace(ws, dev, stream, _lib.moe_block_norm_bwd_workspace_bytes, ctypes.byref(b))
+    _run("moe_block_norm_bwd", dev, stream, ctypes.byref(b), _t.code[like.dtype],
+         _t.code[dx.dtype], *args, ctypes.byref(G), p, nb)
 
 
 def moe_quantize_i8_rows(x, codes, scales, stream=None):
     """8-bit integer codes and per-row fp32 scales of x [rows][cols]."""
-    c = _Call()
-    t = c.torch
     rows, cols = x.shape
-    c.run("moe_quantize_i8_rows", stream, rows, cols,
-          c.take("x", x, rows * cols, (t.float32, t.bfloat16, t.float16)), _dtype_code(x),
-          c.take("codes", codes, rows * cols, (t.int8,)),
-          c.take("scales", scales, rows, (t.float32,)))
+    dev = _device("x", x, 0, _t.act)
+    _run("moe_quantize_i8_rows", dev, stream, rows, cols, x.data_ptr(), _t.code[x.dtype],
+         _addr("codes", codes, rows * cols, _t.i8, dev), _addr("scales", scales, rows, _t.f32, dev))
 
 
 def moe_grouped_gemm_i8_workspace_bytes(rows: int, G: int, K: int, n: int) -> int:
@@ -719,17 +740,18 @@ def moe_grouped_gemm_i8_workspace_bytes(rows: int, G: int, K: int, n: int) -> in
 def moe_grouped_gemm_i8(x, x_scale, w, w_scale, y, offsets=None, ws=None, stream=None):
     """y[r] = x_scale[r] w_scale[e] * (w[e] x[r]) for the rows r of group e:
     x [rows][K] and w [G][n][K] (or [n][K]) codes, y [rows][n]."""
-    c = _Call()
-    t = c.torch
-    (rows, K), n, G = x.shape, w.shape[-2], w.shape[0] if w.dim() == 3 else 1
-    if w.shape[-1] != K:
-        raise ValueError(f"w: rows of {w.shape[-1]} codes, x has rows of {K}")
-    args = (c.take("x", x, rows * K, (t.int8,)), c.take("x_scale", x_scale, rows, (t.float32,)),
-            c.take("offsets", offsets, G + 1, (t.int32,)), c.take("w", w, G * n * K, (t.int8,)),
-            c.take("w_scale", w_scale, G * n, (t.float32,)),
-            c.take("y", y, rows * n, (t.float32, t.bfloat16, t.float16)), _dtype_code(y))
-    nb = _lib.moe_grouped_gemm_i8_workspace_bytes(rows, G, K, n)
-    c.run("moe_grouped_gemm_i8", stream, rows, G, K, n, *args, *c.workspace(nb, ws))
+    rows, K = x.shape
+    shape_w, f32 = w.shape, _t.f32
+    n, G = shape_w[-2], shape_w[0] if len(shape_w) == 3 else 1
+    if shape_w[-1] != K:
+        raise ValueError(f"w: rows of {shape_w[-1]} codes, x has rows of {K}")
+    dev = _device("x", x, 0, _t.i8)
+    args = (x.data_ptr(), _addr("x_scale", x_scale, rows, f32, dev),
+            _addr("offsets", offsets, G + 1, _t.i32, dev), _addr("w", w, 0, _t.i8, dev),
+            _addr("w_scale", w_scale, G * n, f32, dev), _addr("y", y, rows * n, _t.act, dev),
+            _t.code[y.dtype])
+    p, nb, keep = _workspace(ws, dev, stream, _lib.moe_grouped_gemm_i8_workspace_bytes, rows, G, K, n)
+    _run("moe_grouped_gemm_i8", dev, stream, rows, G, K, n, *args, p, nb)
 
 
 def moe_expert_ffn_i8_workspace_bytes(s: MoeShape) -> int:
@@ -742,20 +764,19 @@ def moe_expert_ffn_i8(s: MoeShape, width: int, x_rows, x_scale, offsets, w_gate,
     """Grouped expert FFN with 8-bit integer operands (include/moe.h); codes
     are int8 tensors, scales fp32, y_rows fp32 [T*k][width]."""
     a = a or act()
-    c = _Call()
-    t = c.torch
-    rows, f32, i8 = s.T * s.k, (t.float32,), (t.int8,)
-    args = (c.take("x_rows", x_rows, rows * width, i8), c.take("x_scale", x_scale, rows, f32),
-            c.take("offsets", offsets, s.N + 1, (t.int32,)),
-            c.take("w_gate", w_gate, s.N * s.h * width, i8),
-            c.take("w_up", w_up, s.N * s.h * width, i8),
-            c.take("w_down", w_down, s.N * width * s.h, i8))
-    S = MoeI8Scales(c.take("gate_scale", gate_scale, s.N * s.h, f32),
-                    c.take("up_scale", up_scale, s.N * s.h, f32),
-                    c.take("down_scale", down_scale, s.N * width, f32))
-    y = c.take("y_rows", y_rows, rows * width, f32)
-    c.run("moe_expert_ffn_i8", stream, ctypes.byref(s), width, *args, ctypes.byref(S),
-          ctypes.byref(a), y, *c.workspace(moe_expert_ffn_i8_workspace_bytes(s), ws))
+    rows, f32, i8 = s.T * s.k, _t.f32, _t.i8
+    wn = s.N * s.h * width
+    dev = _device("x_rows", x_rows, rows * width, i8)
+    args = (x_rows.data_ptr(), _addr("x_scale", x_scale, rows, f32, dev),
+            _addr("offsets", offsets, s.N + 1, _t.i32, dev), _addr("w_gate", w_gate, wn, i8, dev),
+            _addr("w_up", w_up, wn, i8, dev), _addr("w_down", w_down, wn, i8, dev))
+    S = MoeI8Scales(_addr("gate_scale", gate_scale, s.N * s.h, f32, dev),
+                    _addr("up_scale", up_scale, s.N * s.h, f32, dev),
+                    _addr("down_scale", down_scale, s.N * width, f32, dev))
+    y = _addr("y_rows", y_rows, rows * width, f32, dev)
+    p, nb, keep = _workspace(ws, dev, stream, _lib.moe_expert_ffn_i8_workspace_bytes, ctypes.byref(s))
+    _run("moe_expert_ffn_i8", dev, stream, ctypes.byref(s), width, *args, ctypes.byref(S),
+         ctypes.byref(a), y, p, nb)
 
 
 def q4_layer(w_route, gate_qs, gate_scales, up_qs, up_scales, down_qs, down_scales,

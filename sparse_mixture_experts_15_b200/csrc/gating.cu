@@ -30,8 +30,9 @@ __device__ __forceinline__ double recip(double x) {
 
 // exp(x) for |x| <= 150: x = n ln 2 + r with |r| <= ln 2 / 2, the Taylor sum of
 // exp(r) to r^10 / 10! (the rest is below 2^-42), times 2^n in the exponent.
-// n is rounded by adding 1.5 2^52, which leaves it in the low word.
-__device__ __forceinline__ double exp_wide(double x) {
+// n is rounded by adding 1.5 2^52, which leaves it in the low word.  zero: the
+// result is 0 (below 2^-1022) whatever x is.
+__device__ __forceinline__ double exp_wide(double x, bool zero = false) {
   constexpr double kRound = 6755399441055744.0;
   const double t = fma(x, 1.4426950408889634, kRound);
   const double r = fma(kRound - t, 0.6931471805599453, x);
@@ -46,7 +47,8 @@ __device__ __forceinline__ double exp_wide(double x) {
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
-  return __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
+  return __hiloint2double(zero ? 0 : __double2hiint(p) + (__double2loint(t) << 20),
+                          __double2loint(p));
 }
 
 // Order of the selection as an unsigned number: larger values first, a NaN
@@ -61,6 +63,11 @@ __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -72,6 +79,13 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+__device__ __forceinline__ void cp_async16(void* smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
+               "l"(g)
+               : "memory");
+}
+
 // A lane's experts: chunks of CH consecutive ones, 32 CH apart, so that a warp
 // reads and writes whole 16-byte pieces of a row where N allows it.
 template <int PER>
@@ -80,9 +94,10 @@ struct Lanes {
   static __device__ __forceinline__ int expert(int lane, int e) {
     return (e / CH) * 32 * CH + lane * CH + e % CH;
   }
+  // wide: the row is 16-byte aligned and N a multiple of 4
   static __device__ __forceinline__ void load(const float* row, int N, int lane, float fill,
-                                              float* v) {
-    if (CH == 4 && N % 4 == 0) {
+                                              bool wide, float* v) {
+    if (CH == 4 && wide) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int j = expert(lane, q * CH);
@@ -95,6 +110,24 @@ struct Lanes {
       for (int e = 0; e < PER; ++e) {
         const int j = expert(lane, e);
         v[e] = j < N ? row[j] : fill;
+      }
+    }
+  }
+  // from a row in shared memory with room for N up to a multiple of 4; 0 past N
+  static __device__ __forceinline__ void load_shared(const float* row, int N, int lane, float* v) {
+#pragma unroll
+    for (int e = 0; e < PER; e += CH) {
+      const int j = expert(lane, e);
+      if constexpr (CH == 4) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (j < N) x = *reinterpret_cast<const float4*>(row + j);
+        v[e] = x.x;
+        v[e + 1] = j + 1 < N ? x.y : 0.0f;
+        v[e + 2] = j + 2 < N ? x.z : 0.0f;
+        v[e + 3] = j + 3 < N ? x.w : 0.0f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[e + i] = j + i < N ? row[j + i] : 0.0f;
       }
     }
   }
@@ -119,6 +152,10 @@ struct Lanes {
 
 struct SelectParams {
   int T, N, k, renorm, sigmoid, n_group, top_group, group_top;
+  int per;        // experts of a group
+  int sub_log;    // log2 of the lanes that read one group
+  uint32_t inv;   // j / per = j inv >> 20, exact for j < 1024
+  int bias_wide;
   float scale;
   const float* logits;
   const float* bias;
@@ -149,7 +186,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
   float* sc = sel_mem + (size_t)wib * 2 * stride;
   uint32_t* od = reinterpret_cast<uint32_t*>(sc + stride);
   float z[PER];
-  L::load(p.logits + t * N, N, lane, -INFINITY, z);
+  L::load(p.logits + t * N, N, lane, -INFINITY, N % 4 == 0, z);
   // scores
   if (p.sigmoid) {
 #pragma unroll
@@ -161,34 +198,34 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
     }
   } else {
     float m = -INFINITY;
-    bool nan = false;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      m = fmaxf(m, z[e]);
-      nan |= z[e] != z[e];
-    }
+    for (int e = 0; e < PER; ++e) m = max_nan(m, z[e]);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    nan = __any_sync(0xffffffffu, nan) || m == INFINITY;
+    for (int o = 16; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const double md = (double)m;
     double x[PER], sum = 0.0;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      // a logit of -infinity scores 0, in a row of nothing else too
-      x[e] = z[e] == -INFINITY ? 0.0 : exp_wide(fmax((double)z[e] - (double)m, -150.0));
+      // 120 below the largest is 0 in fp32, and a logit of -infinity (or a NaN: the
+      // row's factor below) with it
+      x[e] = exp_wide((double)z[e] - md, !(z[e] - m >= -120.0f));
       sum += x[e];
     }
     sum = warp_sum(sum);
-    const double r = sum > 0.0 ? recip(sum) : 0.0;
+    // NaN for a row that holds a NaN or +infinity, 0 for one of nothing but -infinity
+    const double r = m == -INFINITY ? 0.0 : m < INFINITY ? recip(sum) : __hiloint2double(0x7FF80000, 0);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) z[e] = nan ? __uint_as_float(0x7FC00000u) : (float)(x[e] * r);
+    for (int e = 0; e < PER; ++e) z[e] = (float)(x[e] * r);
   }
   if (p.scores) L::store(p.scores + t * N, N, lane, z);
   // the order of the selection, and the scores for the weights
   uint32_t ord[PER];
+  float c[PER];
+  if (p.bias) L::load(p.bias, N, lane, 0.0f, p.bias_wide, c);
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
     const int j = L::expert(lane, e);
-    ord[e] = j < N ? order_of(p.bias ? z[e] + p.bias[j] : z[e]) : 0u;
+    ord[e] = j < N ? order_of(p.bias ? z[e] + c[e] : z[e]) : 0u;
   }
 #pragma unroll
   for (int e = 0; e < PER; e += L::CH) {
@@ -206,14 +243,12 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
   __syncwarp();
   if (p.n_group > 1) {
     // sub lanes of a group read its experts in turn and keep the two best
-    const int G = p.n_group, per = N / G;
-    int sub = 32;
-    while (sub * G > 32) sub >>= 1;
-    const int g = lane / sub;
+    const int G = p.n_group, sub = 1 << p.sub_log, g = lane >> p.sub_log;
     uint32_t b1 = 0u, b2 = 0u;
     if (g < G) {
-      const uint32_t* og = od + g * per;
-      for (int i = lane % sub; i < per; i += sub) {
+      const uint32_t* og = od + g * p.per;
+#pragma unroll 4
+      for (int i = lane & (sub - 1); i < p.per; i += sub) {
         const uint32_t o = og[i];
         b2 = max(b2, min(b1, o));
         b1 = max(b1, o);
@@ -228,17 +263,16 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select(const __grid_cons
     const uint32_t mine =
         order_of(p.group_top == 1 ? value_of(b1) : value_of(b1) + value_of(b2));
     int rank = 0;
+#pragma unroll 4
     for (int h = 0; h < G; ++h) {
-      const uint32_t o = __shfl_sync(0xffffffffu, mine, h * sub);
+      const uint32_t o = __shfl_sync(0xffffffffu, mine, h << p.sub_log);
       rank += o > mine || (o == mine && h < g);
     }
     const uint32_t kept = __ballot_sync(0xffffffffu, g < G && rank < p.top_group);
-    // j / per as a product: exact for j < 1024
-    const uint32_t inv = (1u << 20) / per + 1;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const uint32_t h = L::expert(lane, e) * inv >> 20;
-      if (h < (uint32_t)G && !((kept >> (h * sub)) & 1u)) ord[e] = 0u;
+      const uint32_t h = L::expert(lane, e) * p.inv >> 20;
+      if (h < (uint32_t)G && !((kept >> (h << p.sub_log)) & 1u)) ord[e] = 0u;
     }
   }
   uint32_t best = 0u;
@@ -329,29 +363,40 @@ struct SelectBwdParams {
 // the selected experts give):
 //   renorm: dL/ds_i = scale (da_i - sum_l da_l s_l / S) / S;  else scale da_i
 //   sigmoid: dz_j = g_j s_j (1 - s_j);  softmax: dz_j = s_j (g_j - sum g s)
+// Bound by the rows' bytes.  d_scores is copied to shared memory (cp.async) while
+// the scores are formed, so that it takes no registers and all 4096 tokens of a
+// batch have their warps resident at once.
 template <int PER>
-__global__ void __launch_bounds__(32 * kSelWarps)
+__global__ void __launch_bounds__(32 * kSelWarps, PER <= 28 ? 7 : 6)
     route_select_bwd(const __grid_constant__ SelectBwdParams p) {
   using L = Lanes<PER>;
-  extern __shared__ __align__(16) float sel_mem[];  // per warp: s [N], g [N]
+  extern __shared__ __align__(16) float sel_mem[];  // per warp: s, the slots' part of g [N up to 4]
   pdl_wait();
   pdl_allow_next();
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, N = p.N;
   const int64_t t = (int64_t)blockIdx.x * kSelWarps + wib;
   if (t >= p.T) return;
-  float* ss = sel_mem + (size_t)wib * N * 2;
-  float* gs = ss + N;
-  float z[PER], f[PER];
-  L::load(p.logits + t * N, N, lane, -INFINITY, z);
-  if (p.sigmoid) {
+  const int stride = (N + 3) & ~3;
+  float* ss = sel_mem + (size_t)wib * 2 * stride;
+  float* gs = ss + stride;
+  float z[PER];  // becomes s, then the factor s (1 - s) or s
+  if (p.d_scores && N % 4 == 0) {
+    const float* d = p.d_scores + t * N;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {  // s, and 1 - s without cancellation
-      const float x = expf(-fabsf(z[e]));
-      const float r = 1.0f / (1.0f + x);
-      f[e] = z[e] >= 0.0f ? x * r : r;
-      z[e] = z[e] >= 0.0f ? r : x * r;
+    for (int e = 0; e < PER; e += L::CH) {
+      const int j = L::expert(lane, e);
+      if (L::CH == 4 && j < N) cp_async16(gs + j, d + j);
     }
-  } else {
+  }
+  L::load(p.logits + t * N, N, lane, -INFINITY, N % 4 == 0, z);
+  int idx = lane < p.k ? p.top_idx[t * p.k + lane] : -1;
+  float da = lane < p.k ? p.d_top_w[t * p.k + lane] * p.scale : 0.0f;
+  if (lane < p.k && (idx < 0 || idx >= N)) {
+    record_error(p.status, MOE_ERR_BOUNDS);
+    idx = -1;
+    da = 0.0f;
+  }
+  if (!p.sigmoid) {
     float m = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) m = fmaxf(m, z[e]);
@@ -368,27 +413,42 @@ __global__ void __launch_bounds__(32 * kSelWarps)
     for (int e = 0; e < PER; ++e) z[e] *= r;
   }
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
+  for (int e = 0; e < PER; e += L::CH) {
+    float s[L::CH];
+#pragma unroll
+    for (int i = 0; i < L::CH; ++i) {
+      s[i] = z[e + i];
+      if (p.sigmoid) {  // s, and s (1 - s) without cancellation
+        const float x = expf(-fabsf(s[i])), r = 1.0f / (1.0f + x);
+        s[i] = s[i] >= 0.0f ? r : x * r;
+        z[e + i] = x * r * r;
+      }
+    }
     const int j = L::expert(lane, e);
-    if (j < N) ss[j] = z[e], gs[j] = 0.0f;
+    if (j >= N) continue;
+    if constexpr (L::CH == 4) {
+      *reinterpret_cast<float4*>(ss + j) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < L::CH; ++i)
+        if (j + i < N) ss[j + i] = s[i];
+    }
+    if (L::CH < 4 || N % 4 != 0 || !p.d_scores) {
+#pragma unroll
+      for (int i = 0; i < L::CH; ++i)
+        if (j + i < N) gs[j + i] = p.d_scores ? p.d_scores[t * N + j + i] : 0.0f;
+    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   // the selected experts' part; an index that is there twice counts twice
-  int idx = lane < p.k ? p.top_idx[t * p.k + lane] : -1;
-  float da = lane < p.k ? p.d_top_w[t * p.k + lane] : 0.0f;
-  if (lane < p.k && (idx < 0 || idx >= N)) {
-    record_error(p.status, MOE_ERR_BOUNDS);
-    idx = -1;
-    da = 0.0f;
-  }
-  const float s = idx >= 0 ? ss[idx] : 0.0f;
-  da *= p.scale;
   if (p.renorm) {
-    const float S = warp_sum(s), ds = warp_sum(da * s);
+    const float s = idx >= 0 ? ss[idx] : 0.0f, S = warp_sum(s), ds = warp_sum(da * s);
     da = S == 0.0f || idx < 0 ? 0.0f : (da - ds / S) / S;
   }
   float sum = 0.0f;
   int first = 32;
+#pragma unroll 4
   for (int r = 0; r < p.k; ++r) {
     const int ir = __shfl_sync(0xffffffffu, idx, r);
     const float dr = __shfl_sync(0xffffffffu, da, r);
@@ -397,31 +457,17 @@ __global__ void __launch_bounds__(32 * kSelWarps)
       first = min(first, r);
     }
   }
-  if (idx >= 0 && first == lane) gs[idx] = sum;
+  if (idx >= 0 && first == lane) gs[idx] += sum;
   __syncwarp();
-  float g[PER];
-  if (p.d_scores) {
-    L::load(p.d_scores + t * N, N, lane, 0.0f, g);
-  } else {
-#pragma unroll
-    for (int e = 0; e < PER; ++e) g[e] = 0.0f;
-  }
-#pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    const int j = L::expert(lane, e);
-    if (j < N) g[e] += gs[j];
-  }
-  if (p.sigmoid) {
-#pragma unroll
-    for (int e = 0; e < PER; ++e) g[e] *= z[e] * f[e];
-  } else {
-    float dot = 0.0f;
+  float g[PER], dot = 0.0f;
+  L::load_shared(gs, N, lane, g);
+  if (!p.sigmoid) {
 #pragma unroll
     for (int e = 0; e < PER; ++e) dot = fmaf(g[e], z[e], dot);
     dot = warp_sum(dot);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) g[e] = z[e] * (g[e] - dot);
   }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) g[e] = z[e] * (g[e] - dot);
   L::store(p.dz + t * N, N, lane, g);
 }
 
@@ -477,10 +523,14 @@ bool gating_ok(const moe_shape* s, const moe_gating* g) {
 int launch_select(const moe_shape& s, const moe_gating& g, const float* logits, const float* bias,
                   int32_t* top_idx, float* top_w, float* scores, cudaStream_t st) {
   if (s.T == 0) return MOE_OK;
-  SelectParams p{s.T, s.N, s.k, s.renorm, g.score == MOE_SCORE_SIGMOID, g.n_group, g.top_group,
-                 g.group_top, g.scale, logits, bias, top_idx, top_w, scores};
   // every group kept is no limit
-  if (g.top_group == g.n_group) p.n_group = 1;
+  const int G = g.top_group == g.n_group ? 1 : g.n_group, per = s.N / G;
+  int sub_log = 5;
+  while (G << sub_log > 32) --sub_log;
+  SelectParams p{s.T, s.N, s.k, s.renorm, g.score == MOE_SCORE_SIGMOID, G, g.top_group,
+                 g.group_top, per, sub_log, (1u << 20) / per + 1,
+                 s.N % 4 == 0 && aligned16(bias), g.scale, logits, bias, top_idx,
+                 top_w, scores};
   return by_width<Select>(p, (size_t)kSelWarps * ((s.N + 3) & ~3) * 8, st);
 }
 
@@ -513,7 +563,7 @@ extern "C" int moe_route_select_bwd(const moe_shape* shape, const moe_gating* ga
   if (s.T == 0) return MOE_OK;
   SelectBwdParams p{s.T, s.N, s.k, s.renorm, gating->score == MOE_SCORE_SIGMOID, gating->scale,
                     logits, top_idx, d_top_w, d_scores, dz, status_word()};
-  return by_width<SelectBwd>(p, (size_t)kSelWarps * s.N * 8, as_stream(stream));
+  return by_width<SelectBwd>(p, (size_t)kSelWarps * ((s.N + 3) & ~3) * 8, as_stream(stream));
 }
 
 extern "C" size_t moe_route_scored_workspace_bytes(const moe_shape* shape) {

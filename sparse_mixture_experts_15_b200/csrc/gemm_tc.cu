@@ -665,9 +665,30 @@ int pick_bn(int m_tiles, int64_t max_rows, int G, int cg) {
   return up256 >= 2LL * sm_count() / cg ? 256 : 128;
 }
 
+// 8-bit integers: groups of few rows are bound by the weights' bytes, and every
+// k-block loads BN rows of B whatever the group has, so narrow tiles leave more
+// of the shared memory (and of the L2 reads) to the weights.
+int pick_bn_i8(int m_tiles, int64_t max_rows, int G, int cg) {
+  if (max_rows <= 24LL * G) return 32;
+  if (max_rows <= 56LL * G) return 64;
+  return pick_bn(m_tiles, max_rows, G, cg);
+}
+
 template <int KIND>
 int launch_tc_typed(const TcParams& p, int64_t upper, int bn, int cg, cudaStream_t st) {
   const bool situ = p.mode == MODE_GATEUP && p.act_kind == MOE_ACT_SITU_GLU;
+  if constexpr (KIND == OPS_I8) {
+    if (bn == 32)
+      return cg == 2 ? (situ ? launch_tc<32, 10, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
+                             : launch_tc<32, 10, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st))
+                     : (situ ? launch_tc<32, 9, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
+                             : launch_tc<32, 9, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st));
+    if (bn == 64)
+      return cg == 2 ? (situ ? launch_tc<64, 9, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
+                             : launch_tc<64, 9, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st))
+                     : (situ ? launch_tc<64, 7, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
+                             : launch_tc<64, 7, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st));
+  }
   if (cg == 2) {
     if (bn == 256)
       return situ ? launch_tc<256, 6, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
@@ -726,7 +747,8 @@ int tc_gateup(const int32_t* offsets, int T, int G, const void* X, int64_t x_row
   // CTA pairs take 128 hidden units (64 per CTA) per tile
   const int cg = hidden % 128 == 0 ? 2 : 1;
   const int m_tiles = hidden / (64 * cg);
-  const int bn = pick_bn(m_tiles, max_rows, G, cg);
+  const int bn = kind == OPS_I8 ? pick_bn_i8(m_tiles, max_rows, G, cg)
+                                : pick_bn(m_tiles, max_rows, G, cg);
   const bool u8 = f8 != nullptr;
   if (!make_tmap(&p.maps[0], w_gate, rows_w, K, 64, u8) ||
       !make_tmap(&p.maps[1], w_up, rows_w, K, 64, u8) ||
@@ -773,7 +795,8 @@ int tc_store(const int32_t* offsets, int T, int G, int m_rows, const TcSeg* segs
   // the last tile may be ragged (and the last k-block: the loads fill zeros)
   const int cg = i8 ? (m_rows > kBM ? 2 : 1) : m_rows % (2 * kBM) == 0 ? 2 : 1;
   const int m_tiles = (m_rows + kBM * cg - 1) / (kBM * cg);
-  const int bn = pick_bn(m_tiles, max_rows, G, cg);
+  const int bn = kind == OPS_I8 ? pick_bn_i8(m_tiles, max_rows, G, cg)
+                                : pick_bn(m_tiles, max_rows, G, cg);
   // distinct (pointer, rows, cols, box) tensor maps, at most four
   const void* key_p[4];
   int64_t key_r[4];

@@ -12,9 +12,8 @@
 namespace moe {
 namespace {
 
-// Four quotients x / s to four codes, v[0] lowest: rounded to nearest even and
-// held within +-127 as integers, where a NaN (of an infinity or a NaN over
-// the row's scale) is 0.
+// Four whole numbers to four bytes, v[0] lowest, held within +-127; a NaN (an
+// infinity or a NaN over the row's scale) is 0.
 __device__ __forceinline__ uint32_t pack_i8(const float* v) {
   uint32_t w = 0;
 #pragma unroll
@@ -23,54 +22,128 @@ __device__ __forceinline__ uint32_t pack_i8(const float* v) {
   return w;
 }
 
-// One warp per row of `cols` elements, two passes.  The largest magnitude is
-// taken on the bit patterns (a NaN's are above infinity's), so a row with an
-// infinity or a NaN keeps it in its scale and its products are NaN.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// Sixteen elements of a row to codes.  rint of the rounded quotient x / s: the
+// product by 1 / s is within 2^-16 of that quotient (three roundings of at most
+// 127.5), so only a product within 2^-12 of a tie needs the division.  `slow`:
+// s is subnormal, infinite or NaN.
+__device__ __forceinline__ uint4 codes16(const float* x, float s, float inv, bool slow) {
+  float q[16];
+  bool near = slow;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float v = x[i] * inv;
+    q[i] = rintf(v);
+    near |= fabsf(v - q[i]) > 0.5f - 1.0f / 4096;
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(x[i], s);
+  }
+  return make_uint4(pack_i8(q), pack_i8(q + 4), pack_i8(q + 8), pack_i8(q + 12));
+}
+
+// A team of nt threads (a multiple of 32) takes a row, 16 V elements a thread, held
+// in registers between the row's largest magnitude and the codes: one pass over
+// the bytes, which bound it.  The magnitude is taken on the bit patterns (a NaN's are
+// above infinity's), so a row with an infinity or a NaN keeps it in its scale.
+// V = 0: rows too long for that, read twice by a CTA.
+constexpr int kQuantThreads = 256;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kQuantThreads)
     quant_rows_i8(const T* __restrict__ x, int64_t rows, const int32_t* __restrict__ rows_dev,
-                  int cols, int8_t* __restrict__ codes, float* __restrict__ scales) {
+                  int cols, int nt, int8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ uint32_t largest[2][kQuantThreads / 32];
   pdl_wait();
   pdl_allow_next();
   if (rows_dev) rows = min(rows, (int64_t)max(*rows_dev, 0));
-  const int lane = threadIdx.x & 31;
-  for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; r < rows;
-       r += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+  const int team = threadIdx.x / nt, lane_t = threadIdx.x - team * nt, teams = blockDim.x / nt;
+  int turn = 0;
+  for (int64_t r = (int64_t)blockIdx.x * teams + team; r < rows; r += (int64_t)gridDim.x * teams) {
     const T* xr = x + r * cols;
+    float v[V > 0 ? V : 1][16];
     uint32_t m = 0;
-    for (int c = lane * 8; c < cols; c += 256) {
-      float v[8];
-      load8(xr + c, v);
+    if constexpr (V > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * nt + lane_t) * 16;
+        if (c < cols) {
+          load8(xr + c, v[k]);
+          load8(xr + c + 8, v[k] + 8);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[k][i] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+    } else {
+      for (int c = lane_t * 16; c < cols; c += nt * 16) {
+        load8(xr + c, v[0]);
+        load8(xr + c + 8, v[0] + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[0][i]) & 0x7FFFFFFFu);
+      }
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    const float s = m ? __fdiv_rn(__uint_as_float(m), 127.0f) : 1.0f;
-    for (int c = lane * 8; c < cols; c += 256) {
-      float v[8];
-      load8(xr + c, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], s);
-      *reinterpret_cast<uint2*>(codes + r * cols + c) = make_uint2(pack_i8(v), pack_i8(v + 4));
+    if (nt > 32) {
+      const int w0 = team * (nt / 32);
+      if ((threadIdx.x & 31) == 0) largest[turn][threadIdx.x >> 5] = m;
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(nt) : "memory");
+      for (int w = 0; w < nt / 32; ++w) m = max(m, largest[turn][w0 + w]);
+      turn ^= 1;  // written again only after the next row's barrier
     }
-    if (lane == 0) scales[r] = s;
+    const float s = m ? __fdiv_rn(__uint_as_float(m), 127.0f) : 1.0f, inv = 1.0f / s;
+    const bool slow = !(s >= 1.1754944e-38f && s < INFINITY);
+    if constexpr (V > 0) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (k * nt + lane_t) * 16;
+        if (c < cols)
+          *reinterpret_cast<uint4*>(codes + r * cols + c) = codes16(v[k], s, inv, slow);
+      }
+    } else {
+      for (int c = lane_t * 16; c < cols; c += nt * 16) {
+        load8(xr + c, v[0]);
+        load8(xr + c + 8, v[0] + 8);
+        *reinterpret_cast<uint4*>(codes + r * cols + c) = codes16(v[0], s, inv, slow);
+      }
+    }
+    if (lane_t == 0) scales[r] = s;
   }
 }
 
 int quantize(int64_t rows, const int32_t* rows_dev, int cols, const void* x, int32_t x_dtype,
              int8_t* codes, float* scales, cudaStream_t st) {
   if (rows == 0) return MOE_OK;
-  int64_t grid = (rows + 7) / 8;
-  if (grid > 148 * 16) grid = 148 * 16;
-#define MOE_QUANT(T)                                                                        \
-  do {                                                                                      \
-    MOE_PREFER_SHARED((quant_rows_i8<T>));                                                  \
-    launch_pdl(quant_rows_i8<T>, dim3((unsigned)grid), dim3(256), 0, st,                    \
-               static_cast<const T*>(x), rows, rows_dev, cols, codes, scales);              \
+  const int pieces = cols / 16;
+  const int V = pieces <= kQuantThreads ? 1 : pieces <= 2 * kQuantThreads ? 2
+                : pieces <= 4 * kQuantThreads ? 4 : 0;
+  const int per = V ? (pieces + V - 1) / V : kQuantThreads;
+  const int nt = (per + 31) / 32 * 32, sms = sm_count();
+  int teams = kQuantThreads / nt;
+  if (teams > (rows + sms - 1) / sms) teams = (int)((rows + sms - 1) / sms);
+  int64_t grid = (rows + teams - 1) / teams;
+  if (grid > (int64_t)sms * 16) grid = (int64_t)sms * 16;
+#define MOE_QUANT(T, V)                                                                       \
+  do {                                                                                        \
+    MOE_PREFER_SHARED((quant_rows_i8<T, V>));                                                 \
+    launch_pdl(quant_rows_i8<T, V>, dim3((unsigned)grid), dim3((unsigned)(teams * nt)), 0,    \
+               st, static_cast<const T*>(x), rows, rows_dev, cols, nt, codes, scales);        \
   } while (0)
-  if (x_dtype == MOE_F32) MOE_QUANT(float);
-  else if (x_dtype == MOE_BF16) MOE_QUANT(__nv_bfloat16);
-  else MOE_QUANT(__half);
+#define MOE_QUANT_V(T)           \
+  do {                           \
+    if (V == 1) MOE_QUANT(T, 1); \
+    else if (V == 2) MOE_QUANT(T, 2); \
+    else if (V == 4) MOE_QUANT(T, 4); \
+    else MOE_QUANT(T, 0);        \
+  } while (0)
+  if (x_dtype == MOE_F32) MOE_QUANT_V(float);
+  else if (x_dtype == MOE_BF16) MOE_QUANT_V(__nv_bfloat16);
+  else MOE_QUANT_V(__half);
+#undef MOE_QUANT_V
 #undef MOE_QUANT
   return launch_status();
 }
