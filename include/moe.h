@@ -542,9 +542,9 @@ MOE_API int moe_block_norm_bwd(const moe_block_norm* norm, int32_t dtype, int32_
                                size_t ws_bytes, void* stream);
 
 /* --------------------------------------------------- 8-bit integer products */
-/* Values as codes -127..127 with one fp32 scale per row: s = amax(row) / 127
- * (1 for a zero row), code = x / s rounded to nearest even, each division one
- * fp32 operation.  A row with an infinity or a NaN has that scale, so that
+/* Values as codes -127..127 with one fp32 scale per row: s = amax(row)
+ * times fp32(1/127) (1 for a zero row), code = x / s rounded to nearest even,
+ * the product and the division one fp32 operation each.  A row with an infinity or a NaN has that scale, so that
  * its products are NaN.  x [rows][cols] in x_dtype (MOE_F32, MOE_BF16 or
  * MOE_F16), cols a multiple of 16, codes [rows][cols], scales [rows].  Errors
  * as moe_quantize_e4m3_rows. */

@@ -1,52 +1,100 @@
 // Products of 8-bit integer codes with a scale per token and per channel, and
 // the experts built from them.
 //
-//   x[r][c] ~ s_x[r] q_x[r][c],  s_x = amax(row) / 127,  q = rint(x / s_x)
+//   x[r][c] ~ s_x[r] q_x[r][c],  s_x = amax(row) fp32(1/127),  q = rint(x / s_x)
 //   y[r][j] = s_x[r] s_w[e][j] sum_c q_x[r][c] q_w[e][j][c]     r a row of expert e
 //
 // The sum is an s32 sum of exact products (kind::i8 of the tensor cores), so
 // it does not depend on any order; the only roundings are the conversion of
 // the sum to fp32, the two scalings and the output's type.
 #include "common.cuh"
+#include "pairs.cuh"
+#include "tc_primitives.cuh"
 
 namespace moe {
 namespace {
 
-// Four whole numbers to four bytes, v[0] lowest, held within +-127; a NaN (an
-// infinity or a NaN over the row's scale) is 0.
-__device__ __forceinline__ uint32_t pack_i8(const float* v) {
-  uint32_t w = 0;
+// ------------------------------------------------------------- quantiser
+// Sixteen elements of a row as they are stored: 2 (16-bit) or 4 (fp32) times
+// 16 bytes.
+template <typename T>
+struct Raw {
+  static constexpr int N = sizeof(T) == 4 ? 4 : 2;
+  uint4 w[N];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= (uint32_t)(uint8_t)(int8_t)min(max(__float2int_rn(v[i]), -127), 127) << (8 * i);
-  return w;
-}
+    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  // The largest magnitude as the bits of its fp32 value, at least m.  Magnitudes
+  // are compared as bit patterns, where a NaN's is above infinity's.
+  __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        m = max(m, max(w[i].x & 0x7FFFFFFFu, w[i].y & 0x7FFFFFFFu));
+        m = max(m, max(w[i].z & 0x7FFFFFFFu, w[i].w & 0x7FFFFFFFu));
+      }
+      return m;
+    } else {
+      uint32_t h = 0;  // two 16-bit maxima
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        h = __vmaxu2(h, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu));
+        h = __vmaxu2(h, __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
+      }
+      const uint16_t t = (uint16_t)max(h & 0xFFFFu, h >> 16);
+      return max(m, __float_as_uint(to_f32(*reinterpret_cast<const T*>(&t))));
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+      load8(reinterpret_cast<const T*>(w) + i, v + i);
+  }
+};
 
-// Sixteen elements of a row to codes.  rint of the rounded quotient x / s: the
-// product by 1 / s is within 2^-16 of that quotient (three roundings of at most
-// 127.5), so only a product within 2^-12 of a tie needs the division.  `slow`:
-// s is subnormal, infinite or NaN.
+// Four elements to codes, rint of the rounded quotient x / s.  The product
+// by 1 / s is within 2^-15 of that quotient (three roundings of half a step at
+// most, 2^-24 of values up to 127.5), so only a product within 2^-14 of a tie
+// needs the division.  Rounding is by
+// adding 1.5 2^23, which leaves the whole number in the low byte; within a row of
+// a normal scale no quotient rounds above 127.  `slow`: s is subnormal, infinite
+// or NaN; codes are then held within +-127, and a NaN (an infinity or a NaN over
+// the scale) is 0.
+__device__ __forceinline__ uint32_t codes4(const float* x, float s, float inv, bool slow) {
+  constexpr float kRound = 12582912.0f;
+  uint32_t q[4];
+  float off = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const Pair v = mul2(pair(x[i], x[i + 1]), pair(inv, inv)), r = add2(v, pair(kRound, kRound));
+    const float2 w = parts(r);
+    q[i] = __float_as_uint(w.x);
+    q[i + 1] = __float_as_uint(w.y);
+    const float2 d = parts(fma2(add2(r, pair(-kRound, -kRound)), pair(-1.0f, -1.0f), v));
+    off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+  }
+  if (slow || off > 0.5f - 1.0f / 16384) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = (uint32_t)min(max(__float2int_rn(__fdiv_rn(x[i], s)), -127), 127);
+  }
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
 __device__ __forceinline__ uint4 codes16(const float* x, float s, float inv, bool slow) {
-  float q[16];
-  bool near = slow;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float v = x[i] * inv;
-    q[i] = rintf(v);
-    near |= fabsf(v - q[i]) > 0.5f - 1.0f / 4096;
-  }
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(x[i], s);
-  }
-  return make_uint4(pack_i8(q), pack_i8(q + 4), pack_i8(q + 8), pack_i8(q + 12));
+  return make_uint4(codes4(x, s, inv, slow), codes4(x + 4, s, inv, slow),
+                    codes4(x + 8, s, inv, slow), codes4(x + 12, s, inv, slow));
 }
 
 // A team of nt threads (a multiple of 32) takes a row, 16 V elements a thread, held
-// in registers between the row's largest magnitude and the codes: one pass over
-// the bytes, which bound it.  The magnitude is taken on the bit patterns (a NaN's are
-// above infinity's), so a row with an infinity or a NaN keeps it in its scale.
-// V = 0: rows too long for that, read twice by a CTA.
+// as stored between the row's largest magnitude and the codes, with the next
+// row's loads in flight: one pass over the bytes, which bound it.  A row with an
+// infinity or a NaN keeps it in its scale.  V = 0: rows too long for that, read
+// twice by a CTA.
 constexpr int kQuantThreads = 256;
 
 template <typename T, int V>
@@ -58,33 +106,33 @@ __global__ void __launch_bounds__(kQuantThreads)
   pdl_allow_next();
   if (rows_dev) rows = min(rows, (int64_t)max(*rows_dev, 0));
   const int team = threadIdx.x / nt, lane_t = threadIdx.x - team * nt, teams = blockDim.x / nt;
+  constexpr int H = V > 0 ? V : 1;
+  Raw<T> now[H], next[H];
+  const int64_t step = (int64_t)gridDim.x * teams;
+  int64_t r = (int64_t)blockIdx.x * teams + team;
+  const T* src = x + r * cols + lane_t * 16;  // the next row to fetch
+  auto fetch = [&](int64_t row, Raw<T>* o) {
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      if (row < rows && (k * nt + lane_t) * 16 < cols) o[k].load(src + k * nt * 16);
+      else o[k].zero();
+    }
+    src += step * cols;
+  };
+  if (V > 0) fetch(r, next);
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * teams + team; r < rows; r += (int64_t)gridDim.x * teams) {
-    const T* xr = x + r * cols;
-    float v[V > 0 ? V : 1][16];
+  for (; r < rows; r += step) {
     uint32_t m = 0;
     if constexpr (V > 0) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = (k * nt + lane_t) * 16;
-        if (c < cols) {
-          load8(xr + c, v[k]);
-          load8(xr + c + 8, v[k] + 8);
-        } else {
+      for (int k = 0; k < H; ++k) now[k] = next[k];
+      fetch(r + step, next);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[k][i] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+      for (int k = 0; k < H; ++k) m = now[k].largest(m);
     } else {
       for (int c = lane_t * 16; c < cols; c += nt * 16) {
-        load8(xr + c, v[0]);
-        load8(xr + c + 8, v[0] + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[0][i]) & 0x7FFFFFFFu);
+        now[0].load(x + r * cols + c);
+        m = now[0].largest(m);
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
@@ -92,23 +140,25 @@ __global__ void __launch_bounds__(kQuantThreads)
       const int w0 = team * (nt / 32);
       if ((threadIdx.x & 31) == 0) largest[turn][threadIdx.x >> 5] = m;
       asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(nt) : "memory");
-      for (int w = 0; w < nt / 32; ++w) m = max(m, largest[turn][w0 + w]);
+      const int lane = threadIdx.x & 31;
+      m = __reduce_max_sync(0xffffffffu, lane < nt / 32 ? largest[turn][w0 + lane] : 0u);
       turn ^= 1;  // written again only after the next row's barrier
     }
-    const float s = m ? __fdiv_rn(__uint_as_float(m), 127.0f) : 1.0f, inv = 1.0f / s;
+    const float s = m ? __fmul_rn(__uint_as_float(m), 1.0f / 127.0f) : 1.0f, inv = 1.0f / s;
     const bool slow = !(s >= 1.1754944e-38f && s < INFINITY);
+    float v[16];
     if constexpr (V > 0) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
+      for (int k = 0; k < H; ++k) {
         const int c = (k * nt + lane_t) * 16;
-        if (c < cols)
-          *reinterpret_cast<uint4*>(codes + r * cols + c) = codes16(v[k], s, inv, slow);
+        now[k].values(v);
+        if (c < cols) *reinterpret_cast<uint4*>(codes + r * cols + c) = codes16(v, s, inv, slow);
       }
     } else {
       for (int c = lane_t * 16; c < cols; c += nt * 16) {
-        load8(xr + c, v[0]);
-        load8(xr + c + 8, v[0] + 8);
-        *reinterpret_cast<uint4*>(codes + r * cols + c) = codes16(v[0], s, inv, slow);
+        now[0].load(x + r * cols + c);
+        now[0].values(v);
+        *reinterpret_cast<uint4*>(codes + r * cols + c) = codes16(v, s, inv, slow);
       }
     }
     if (lane_t == 0) scales[r] = s;
@@ -159,6 +209,176 @@ bool gemm_sizes_ok(int32_t rows, int32_t G, int32_t K, int32_t n) {
          (int64_t)G * n < ((int64_t)1 << 31);
 }
 
+// -------------------------------------------------------------- few rows
+// The product for at most 4 rows in all, bound by the weights' bytes: each warp
+// streams whole weight rows, 16 bytes a lane, four channels at once, and forms
+// four products an instruction (dp4a) with the token rows, which the CTA holds in
+// shared memory; a channel's sum is one integer reduction of the warp.  The
+// channels of the groups that have rows are dealt to the CTAs (one per SM) and
+// their warps in equal shares.  With one group a CTA knows its share at once and
+// starts its fetch to L2 before it waits for the previous kernel (a fetch to L2
+// holds nothing that could grow stale).  Rows x 4096 -> 14336 in us, here and with
+// the tensor cores: 1 row 12.1 and 14.2, 4 rows 15.0 and 18.2.
+constexpr int kFewRows = 4, kFewThreads = 1024, kFewSmem = 200 * 1024;
+constexpr int kFewSteps = 1;  // 512-byte steps of a weight row loaded at once
+
+struct FewParams {
+  int rows, G, K, n;
+  const int8_t *x, *w;
+  const float *x_scale, *w_scale;
+  const int32_t* offsets;
+  void* y;
+  int* status;
+};
+
+__device__ __forceinline__ uint4 stream16(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int dot16(uint4 a, uint4 b, int c) {
+  c = __dp4a((int)a.x, (int)b.x, c);
+  c = __dp4a((int)a.y, (int)b.y, c);
+  c = __dp4a((int)a.z, (int)b.z, c);
+  return __dp4a((int)a.w, (int)b.w, c);
+}
+
+// Channels ch .. ch + nch - 1 (nch <= 4) of one group for R token rows in xs [R][K].
+template <int R, typename TY>
+__device__ __forceinline__ void few_dots(const FewParams& p, int g, int ch, int nch, int row0,
+                                         int rows, const int8_t* xs) {
+  const int lane = threadIdx.x & 31;
+  const int8_t* w[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) w[c] = p.w + ((size_t)g * p.n + ch + min(c, nch - 1)) * p.K;
+  int acc[4][R];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[c][r] = 0;
+  constexpr int U = kFewSteps;
+  for (int k = lane * 16; k < p.K; k += U * 512) {
+    uint4 v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v[u][c] = c < nch && k + u * 512 < p.K ? stream16(w[c] + k + u * 512) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k + u * 512 >= p.K) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 x = *reinterpret_cast<const uint4*>(xs + (size_t)r * p.K + k + u * 512);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c][r] = dot16(v[u][c], x, acc[c][r]);
+      }
+    }
+  }
+  __syncwarp();
+  int mine = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int s = __reduce_add_sync(0xffffffffu, acc[c][r]);
+      if (lane == c * R + r) mine = s;
+    }
+  const int c = lane / R, r = lane % R;
+  if (c < nch && r < rows)
+    static_cast<TY*>(p.y)[(size_t)(row0 + r) * p.n + ch + c] = from_f32<TY>(
+        __int2float_rn(mine) * p.w_scale[(size_t)g * p.n + ch + c] * p.x_scale[row0 + r]);
+}
+
+template <typename TY>
+__global__ void __launch_bounds__(kFewThreads, 1) i8_few_rows(const __grid_constant__ FewParams p) {
+  extern __shared__ __align__(16) int8_t xs[];  // [rows up to a power of 2][K]
+  __shared__ int grp[kFewRows], beg[kFewRows], cnt[kFewRows], groups;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.G == 1) {
+    const int64_t lo = (int64_t)p.n * blockIdx.x / gridDim.x;
+    const int64_t hi = (int64_t)p.n * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t c = lo + tid; c < hi; c += kFewThreads) tc::l2_prefetch(p.w + c * p.K, p.K);
+  }
+  pdl_wait();
+  pdl_allow_next();
+  if (warp == 0) {  // the groups that have rows: at most p.rows of them, in order
+    int found = 0;
+    for (int base = 0; base < p.G; base += 32) {
+      const int g = base + lane;
+      int b = 0, c = 0;
+      if (g < p.G) {
+        b = p.offsets ? p.offsets[g] : 0;
+        c = (p.offsets ? p.offsets[g + 1] : p.rows) - b;
+        if (c < 0 || b < 0 || b > p.rows || c > p.rows - b) {  // rows outside the buffers
+          record_error(p.status, MOE_ERR_BOUNDS);
+          c = 0;
+        }
+      }
+      const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
+      const int at = found + __popc(some & ((1u << lane) - 1));
+      // offsets that run back and forth could name more groups than there are rows
+      if (c > 0 && at < kFewRows) grp[at] = g, beg[at] = b, cnt[at] = c;
+      found += __popc(some);
+    }
+    if (lane == 0) {
+      if (found > kFewRows) record_error(p.status, MOE_ERR_BOUNDS);
+      groups = min(found, kFewRows);
+    }
+  }
+  __syncthreads();
+  const int64_t all = (int64_t)groups * p.n;
+  int64_t at = all * blockIdx.x / gridDim.x;
+  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  while (at < end) {
+    const int a = (int)(at / p.n), ch0 = (int)(at - (int64_t)a * p.n);
+    const int seg = (int)min((int64_t)(p.n - ch0), end - at);
+    const int rows = cnt[a], row0 = beg[a];
+    __syncthreads();  // the last segment's rows are no longer read
+    const int R = rows > 2 ? 4 : rows, per = p.K / 16;
+    for (int i = tid; i < R * per; i += kFewThreads) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row0 * p.K) + i;
+      reinterpret_cast<uint4*>(xs)[i] = i < rows * per ? *src : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    constexpr int W = kFewThreads / 32;
+    const int lo = ch0 + (int)((int64_t)seg * warp / W);
+    const int hi = ch0 + (int)((int64_t)seg * (warp + 1) / W);
+    for (int ch = lo; ch < hi; ch += 4) {
+      const int nch = min(4, hi - ch);
+      if (R == 1) few_dots<1, TY>(p, grp[a], ch, nch, row0, rows, xs);
+      else if (R == 2) few_dots<2, TY>(p, grp[a], ch, nch, row0, rows, xs);
+      else few_dots<4, TY>(p, grp[a], ch, nch, row0, rows, xs);
+    }
+    at += seg;
+  }
+}
+
+// Shared memory of i8_few_rows, or 0 where it does not fit.
+size_t few_smem(int rows, int K) {
+  if (rows > kFewRows) return 0;
+  const size_t b = (size_t)(rows > 2 ? 4 : rows) * K;
+  return b <= kFewSmem ? b : 0;
+}
+
+template <typename TY>
+int launch_few(const FewParams& p, size_t smem, cudaStream_t st) {
+  static std::atomic<bool> configured[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !device_slot(dev)) return MOE_ERR_CUDA;
+  if (needs_setup(configured, dev)) {
+    if (cudaFuncSetAttribute(i8_few_rows<TY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kFewSmem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    mark_setup(configured, dev);
+  }
+  MOE_PREFER_SHARED((i8_few_rows<TY>));
+  launch_pdl(i8_few_rows<TY>, dim3((unsigned)sm_count()), dim3(kFewThreads), smem, st, p);
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -192,11 +412,18 @@ extern "C" int moe_grouped_gemm_i8(int32_t rows, int32_t G, int32_t K, int32_t n
   if (!x || !x_scale || !y || !aligned16(x) || !aligned4(x_scale) || !aligned16(y))
     return MOE_ERR_INVALID_ARG;
   (void)ws, (void)ws_bytes;
+  cudaStream_t st = as_stream(stream);
+  if (const size_t smem = few_smem(rows, K)) {
+    const FewParams p{rows, G, K, n, x, w, x_scale, w_scale, offsets, y, status_word()};
+    return y_dtype == MOE_F32    ? launch_few<float>(p, smem, st)
+           : y_dtype == MOE_BF16 ? launch_few<__nv_bfloat16>(p, smem, st)
+                                 : launch_few<__half>(p, smem, st);
+  }
   TcF8 ops{{w_scale, nullptr}, x_scale, OPS_I8};
   TcSeg seg{w, (int64_t)G * n, K, 0, x, rows, K, 0};
   const int mode = y_dtype == MOE_F32 ? MODE_STORE_F32
                    : y_dtype == MOE_BF16 ? MODE_STORE_BF16 : MODE_STORE_F16;
-  return tc_store(offsets, rows, G, n, &seg, 1, y, mode, n, as_stream(stream), &ops);
+  return tc_store(offsets, rows, G, n, &seg, 1, y, mode, n, st, &ops);
 }
 
 // H bf16 [T*k][h], its codes [T*k][h] and their row scales [T*k]

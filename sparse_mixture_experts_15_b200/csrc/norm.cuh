@@ -14,6 +14,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "pairs.cuh"
 #include "tc_primitives.cuh"
 
 namespace moe {
@@ -23,33 +24,6 @@ constexpr int kNormMaxD = 16384;       // a cluster of 4 CTAs of 256 threads x 1
 constexpr int kNormSmem = 200 * 1024;  // dynamic shared memory of an SM that the CTAs take, at most
 
 namespace {
-
-// ---------------------------------------------------------- pairs of fp32
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float a, float b) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 parts(Pair p) {
-  float2 v;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float sum2(Pair p) {
-  const float2 v = parts(p);
-  return v.x + v.y;
-}
 
 // Two values of 16 bits (the low half first) as a pair.
 template <typename T>

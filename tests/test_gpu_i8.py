@@ -25,7 +25,7 @@ def quant_ref(x):
     x = x.astype(np.float32)
     amax = np.abs(x).max(1, keepdims=True)
     with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
-        s = np.where(amax == 0, np.float32(1), amax / np.float32(127)).astype(np.float32)
+        s = np.where(amax == 0, np.float32(1), amax * np.float32(1 / 127)).astype(np.float32)
         q = np.clip(np.rint(x / s), -127, 127)
     return np.nan_to_num(q).astype(np.int8), s[:, 0]
 
@@ -54,6 +54,18 @@ def test_quantize_rows_exactly(rows, cols, dtype):
     q, s = quant_ref(t.float().cpu().numpy())
     assert np.array_equal(scales.cpu().numpy().view(np.uint32), s.view(np.uint32))
     assert np.array_equal(codes.cpu().numpy(), q)
+
+
+def test_quantize_many_rows_exactly():
+    """Enough elements that hundreds lie within 2^-14 of a tie between two
+    codes, where the product by the reciprocal cannot decide."""
+    x = torch.randn(6000, 1040, generator=torch.Generator(device="cuda").manual_seed(1),
+                    device="cuda")
+    codes, scales = quant(x)
+    amax = x.abs().amax(1)
+    s = amax * torch.full_like(amax, float(np.float32(1 / 127)))
+    assert torch.equal(scales, s)
+    assert torch.equal(codes.float(), torch.round(x / s[:, None]))
 
 
 def test_quantize_keeps_infinities_and_nan_in_the_scale():
