@@ -612,8 +612,7 @@ def _device(what, t, n, dtypes):
 
 def _run(where, dev, stream, *args):
     """The C call on device dev and its current stream unless one is given."""
-    if stream is None:
-        stream = _t.raw_stream(dev)
+    stream = _t.raw_stream(dev) if stream is None else int(stream)
     if _t.torch.cuda.current_device() == dev:
         rc = getattr(_lib, where)(*args, stream)
     else:

@@ -88,6 +88,10 @@ def check(z, bias, k, sigmoid, **kw):
     # division and the product by the scale: 9 roundings, and 1 for their products
     assert np.all((np.abs(w - ref_w) <= 10 * U * np.abs(ref_w) + 8 * tiny) | np.isnan(ref_w))
     assert np.all(np.isnan(w) == np.isnan(ref_w))
+    idx2, w2, _ = run(z, bias, k, sigmoid, scores=False, **kw)   # without the scores
+    assert np.array_equal(idx2, ref_idx)
+    assert np.all((np.abs(w2 - ref_w) <= 10 * U * np.abs(ref_w) + 8 * tiny) | np.isnan(ref_w))
+    assert np.all(np.isnan(w2) == np.isnan(ref_w))
     return idx, w, sc
 
 
@@ -125,6 +129,19 @@ def test_many_tokens_select_exactly():
     b = (rng.standard_normal(256) * 0.05).astype(np.float32)
     check(z, b, 8, True, G=8, top_group=4, group_top=2)
     check(z[:6000], b, 8, False)
+
+
+def test_values_a_rounding_apart_are_ordered():
+    """Rows whose scores differ in their last bits, group scores among them, so
+    that every decision hangs on them."""
+    rng = np.random.default_rng(9)
+    z = (0.7 + rng.integers(-40, 40, (3000, 128)) * 2.0 ** -23).astype(np.float32)
+    z[1000:2000] = (-3.0 + rng.integers(-9, 9, (1000, 128)) * 2.0 ** -21).astype(np.float32)
+    z[2000:, ::2] = rng.standard_normal((1000, 64)).astype(np.float32)
+    check(z, None, 8, True)
+    check(z, None, 8, True, G=8, top_group=3, group_top=2)
+    b = (rng.integers(-8, 8, 128) * 2.0 ** -24).astype(np.float32)
+    check(z, b, 5, True, G=16, top_group=4, group_top=1)
 
 
 def test_ties_go_to_the_lower_expert():
