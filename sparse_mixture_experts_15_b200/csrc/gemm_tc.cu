@@ -688,7 +688,11 @@ int pick_bn(int m_tiles, int64_t max_rows, int G, int cg) {
 
 // 8-bit integers: groups of few rows are bound by the weights' bytes, and every
 // k-block loads BN rows of B whatever the group has, so narrow tiles leave more
-// of the shared memory (and of the L2 reads) to the weights.
+// of the shared memory (and of the L2 reads) to the weights, as long as they
+// hold most groups whole (a second tile reads the weights again).  In us, 32 /
+// 64 / 128 wide: 8 rows 4096 -> 14336 14.2 / 16.4 / 19.6; 512 rows in 64 groups
+// 4096 -> 1536 68.7 / 69.8 / 70.8; 1531 rows in 64 groups 1040 -> 2056 45.6 (on
+// pairs) / 33.5 / 40.0.
 int pick_bn_i8(int m_tiles, int64_t max_rows, int G, int cg) {
   if (max_rows <= 8LL * G) return 32;
   if (max_rows <= 32LL * G) return 64;
@@ -698,17 +702,17 @@ int pick_bn_i8(int m_tiles, int64_t max_rows, int G, int cg) {
 template <int KIND>
 int launch_tc_typed(const TcParams& p, int64_t upper, int bn, int cg, cudaStream_t st) {
   const bool situ = p.mode == MODE_GATEUP && p.act_kind == MOE_ACT_SITU_GLU;
+  // the gate/up products of 8-bit integers run on pairs only
+  constexpr int SITU1 = KIND == OPS_I8 ? MOE_ACT_SWIGLU : MOE_ACT_SITU_GLU;
   if constexpr (KIND == OPS_I8) {
     if (bn == 32)
       return cg == 2 ? (situ ? launch_tc<32, 10, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
                              : launch_tc<32, 10, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st))
-                     : (situ ? launch_tc<32, 9, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
-                             : launch_tc<32, 9, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st));
+                     : launch_tc<32, 9, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st);
     if (bn == 64)
       return cg == 2 ? (situ ? launch_tc<64, 9, MOE_ACT_SITU_GLU, 2, KIND>(p, upper, st)
                              : launch_tc<64, 9, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st))
-                     : (situ ? launch_tc<64, 7, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
-                             : launch_tc<64, 7, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st));
+                     : launch_tc<64, 7, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st);
   }
   if (cg == 2) {
     if (bn == 256)
@@ -718,9 +722,9 @@ int launch_tc_typed(const TcParams& p, int64_t upper, int bn, int cg, cudaStream
                 : launch_tc<128, 8, MOE_ACT_SWIGLU, 2, KIND>(p, upper, st);
   }
   if (bn == 256)
-    return situ ? launch_tc<256, 4, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
+    return situ ? launch_tc<256, 4, SITU1, 1, KIND>(p, upper, st)
                 : launch_tc<256, 4, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st);
-  return situ ? launch_tc<128, 6, MOE_ACT_SITU_GLU, 1, KIND>(p, upper, st)
+  return situ ? launch_tc<128, 6, SITU1, 1, KIND>(p, upper, st)
               : launch_tc<128, 6, MOE_ACT_SWIGLU, 1, KIND>(p, upper, st);
 }
 

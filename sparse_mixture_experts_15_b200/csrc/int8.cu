@@ -210,7 +210,7 @@ bool gemm_sizes_ok(int32_t rows, int32_t G, int32_t K, int32_t n) {
 }
 
 // -------------------------------------------------------------- few rows
-// The product for at most 4 rows in all, bound by the weights' bytes: each warp
+// The product for at most 2 rows in all, bound by the weights' bytes: each warp
 // streams whole weight rows, 16 bytes a lane, four channels at once, and forms
 // four products an instruction (dp4a) with the token rows, which the CTA holds in
 // shared memory; a channel's sum is one integer reduction of the warp.  The
@@ -218,9 +218,8 @@ bool gemm_sizes_ok(int32_t rows, int32_t G, int32_t K, int32_t n) {
 // their warps in equal shares.  With one group a CTA knows its share at once and
 // starts its fetch to L2 before it waits for the previous kernel (a fetch to L2
 // holds nothing that could grow stale).  Rows x 4096 -> 14336 in us, here and with
-// the tensor cores: 1 row 12.1 and 14.2, 4 rows 15.0 and 18.2.
-constexpr int kFewRows = 4, kFewThreads = 1024, kFewSmem = 200 * 1024;
-constexpr int kFewSteps = 1;  // 512-byte steps of a weight row loaded at once
+// the tensor cores: 1 row 11.7 and 14.4, 2 rows 11.9 and 14.4 (4 rows: 15.0 and 14.8).
+constexpr int kFewRows = 2, kFewThreads = 1024, kFewSmem = 200 * 1024;
 
 struct FewParams {
   int rows, G, K, n;
@@ -245,10 +244,10 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int c) {
   return __dp4a((int)a.w, (int)b.w, c);
 }
 
-// Channels ch .. ch + nch - 1 (nch <= 4) of one group for R token rows in xs [R][K].
+// Channels ch .. ch + nch - 1 (nch <= 4) of one group for its R rows, in xs [R][K].
 template <int R, typename TY>
 __device__ __forceinline__ void few_dots(const FewParams& p, int g, int ch, int nch, int row0,
-                                         int rows, const int8_t* xs) {
+                                         const int8_t* xs) {
   const int lane = threadIdx.x & 31;
   const int8_t* w[4];
 #pragma unroll
@@ -258,23 +257,15 @@ __device__ __forceinline__ void few_dots(const FewParams& p, int g, int ch, int 
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[c][r] = 0;
-  constexpr int U = kFewSteps;
-  for (int k = lane * 16; k < p.K; k += U * 512) {
-    uint4 v[U][4];
+  for (int k = lane * 16; k < p.K; k += 512) {
+    uint4 v[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int c = 0; c < 4; ++c) v[c] = c < nch ? stream16(w[c] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        v[u][c] = c < nch && k + u * 512 < p.K ? stream16(w[c] + k + u * 512) : make_uint4(0, 0, 0, 0);
+    for (int r = 0; r < R; ++r) {
+      const uint4 x = *reinterpret_cast<const uint4*>(xs + (size_t)r * p.K + k);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k + u * 512 >= p.K) break;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint4 x = *reinterpret_cast<const uint4*>(xs + (size_t)r * p.K + k + u * 512);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c][r] = dot16(v[u][c], x, acc[c][r]);
-      }
+      for (int c = 0; c < 4; ++c) acc[c][r] = dot16(v[c], x, acc[c][r]);
     }
   }
   __syncwarp();
@@ -287,14 +278,14 @@ __device__ __forceinline__ void few_dots(const FewParams& p, int g, int ch, int 
       if (lane == c * R + r) mine = s;
     }
   const int c = lane / R, r = lane % R;
-  if (c < nch && r < rows)
+  if (c < nch)
     static_cast<TY*>(p.y)[(size_t)(row0 + r) * p.n + ch + c] = from_f32<TY>(
         __int2float_rn(mine) * p.w_scale[(size_t)g * p.n + ch + c] * p.x_scale[row0 + r]);
 }
 
 template <typename TY>
 __global__ void __launch_bounds__(kFewThreads, 1) i8_few_rows(const __grid_constant__ FewParams p) {
-  extern __shared__ __align__(16) int8_t xs[];  // [rows up to a power of 2][K]
+  extern __shared__ __align__(16) int8_t xs[];  // [rows of a group][K]
   __shared__ int grp[kFewRows], beg[kFewRows], cnt[kFewRows], groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (p.G == 1) {
@@ -337,20 +328,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) i8_few_rows(const __grid_const
     const int seg = (int)min((int64_t)(p.n - ch0), end - at);
     const int rows = cnt[a], row0 = beg[a];
     __syncthreads();  // the last segment's rows are no longer read
-    const int R = rows > 2 ? 4 : rows, per = p.K / 16;
-    for (int i = tid; i < R * per; i += kFewThreads) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)row0 * p.K) + i;
-      reinterpret_cast<uint4*>(xs)[i] = i < rows * per ? *src : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = tid; i < rows * (p.K / 16); i += kFewThreads)
+      reinterpret_cast<uint4*>(xs)[i] =
+          reinterpret_cast<const uint4*>(p.x + (size_t)row0 * p.K)[i];
     __syncthreads();
     constexpr int W = kFewThreads / 32;
     const int lo = ch0 + (int)((int64_t)seg * warp / W);
     const int hi = ch0 + (int)((int64_t)seg * (warp + 1) / W);
     for (int ch = lo; ch < hi; ch += 4) {
       const int nch = min(4, hi - ch);
-      if (R == 1) few_dots<1, TY>(p, grp[a], ch, nch, row0, rows, xs);
-      else if (R == 2) few_dots<2, TY>(p, grp[a], ch, nch, row0, rows, xs);
-      else few_dots<4, TY>(p, grp[a], ch, nch, row0, rows, xs);
+      if (rows == 1) few_dots<1, TY>(p, grp[a], ch, nch, row0, xs);
+      else few_dots<2, TY>(p, grp[a], ch, nch, row0, xs);
     }
     at += seg;
   }
@@ -359,7 +347,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) i8_few_rows(const __grid_const
 // Shared memory of i8_few_rows, or 0 where it does not fit.
 size_t few_smem(int rows, int K) {
   if (rows > kFewRows) return 0;
-  const size_t b = (size_t)(rows > 2 ? 4 : rows) * K;
+  const size_t b = (size_t)rows * K;
   return b <= kFewSmem ? b : 0;
 }
 
