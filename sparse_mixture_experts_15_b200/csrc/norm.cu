@@ -23,13 +23,57 @@ struct NormFwd {
   int* status;
 };
 
+// A sum over the threads of a row: lanes by a shuffle tree, the team's warps in
+// order from shared memory, then the CTAs of the cluster in rank order through
+// distributed shared memory.  Two buffers taken in turn: a thread writes a buffer
+// again only after a barrier that every reader of its last contents has reached.
+struct RowSumMem {
+  float warp_part[2][kNormThreads / 32];  // by warp of the CTA
+  float rank_part[2][4];
+};
+struct RowSum {
+  RowSumMem* m;
+  int team, nt, warps, C;  // warps: of this team
+  int turn;
+};
+__device__ __forceinline__ float row_sum(RowSum& r, float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int b = r.turn;
+  if (r.warps > 1) {
+    if ((threadIdx.x & 31) == 0) r.m->warp_part[b][threadIdx.x >> 5] = v;
+    team_sync(r.team, r.nt);
+    const float* p = &r.m->warp_part[b][r.team * r.warps];
+    v = p[0];
+#pragma unroll
+    for (int i = 1; i < kNormThreads / 32; ++i) {
+      if (i >= r.warps) break;
+      v += p[i];
+    }
+  }
+  if (r.C > 1) {  // warps > 1: rows this wide fill their teams
+    if ((int)threadIdx.x < r.C) {
+      uint32_t a;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(a)
+                   : "r"(smem_addr(&r.m->rank_part[b][blockIdx.x % r.C])), "r"(threadIdx.x));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+    }
+    cluster_barrier();
+    v = r.m->rank_part[b][0];
+    for (int c = 1; c < r.C; ++c) v += r.m->rank_part[b][c];
+  }
+  r.turn = b ^ 1;
+  return v;
+}
+
 // HASY: a block's output comes in (POST: normed first; FULL: gated by element;
 // a channel's gate is part of coef, a token's of the row's factor).
 template <typename T, int S, bool HASY, bool POST, bool FULL, bool PRE>
 __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
     block_norm_fwd(const __grid_constant__ NormFwd p) {
   extern __shared__ __align__(128) char ring_mem[];
-  __shared__ SumBuffers sum_mem;
+  __shared__ RowSumMem sum_mem;
   __shared__ uint64_t full_bar[kMaxTeams][S];
   constexpr int W = chunk_width<T, T>(), NV = kCols / W, E = sizeof(T), A = 1 + HASY + FULL;
   const int nt = p.nt;
@@ -86,9 +130,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
         Pair a = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) a = fma2(y[k], y[k], a);
-        float ss[1] = {sum2(a)};
-        row_sum<1>(sums, ss);
-        r *= rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
+        r *= rsqrtf(fmaf(row_sum(sums, sum2(a)), p.inv_d, p.eps));
       }
       const Pair rr = pair(r, r);
 #pragma unroll
@@ -107,9 +149,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
       Pair a = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) a = fma2(x[k], x[k], a);
-      float ss[1] = {sum2(a)};
-      row_sum<1>(sums, ss);
-      const float r1 = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
+      const float r1 = rsqrtf(fmaf(row_sum(sums, sum2(a)), p.inv_d, p.eps));
       const Pair rr = pair(r1, r1);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = mul2(mul2(x[k], rr), wpre[k]);

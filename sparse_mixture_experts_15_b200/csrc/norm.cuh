@@ -212,71 +212,6 @@ __device__ __forceinline__ void cluster_barrier() {
                ::: "memory");
 }
 
-// Sums of K values over the threads of a row: lanes by a shuffle tree, the
-// team's warps in order from shared memory, then the CTAs of the cluster in
-// rank order through distributed shared memory.  Two buffers taken in turn:
-// a thread writes a buffer again only after a barrier that every reader of
-// its last contents has reached.
-struct SumBuffers {
-  float4 warp_part[2][kNormThreads / 32];  // by warp of the CTA
-  float4 rank_part[2][4];
-};
-struct RowSum {
-  SumBuffers* m;
-  int team, nt, warps, C;     // warps: of this team
-  int turn;
-};
-
-template <int K>
-__device__ __forceinline__ void row_sum(RowSum& r, float* v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  const int b = r.turn;
-  if (r.warps > 1) {
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0)
-      r.m->warp_part[b][w] = make_float4(v[0], K > 1 ? v[1] : 0.0f, K > 2 ? v[2] : 0.0f, 0.0f);
-    asm volatile("bar.sync %0, %1;" ::"r"(r.team + 1), "r"(r.nt) : "memory");
-    const float4* p = &r.m->warp_part[b][r.team * r.warps];
-    float4 a = p[0];
-#pragma unroll
-    for (int i = 1; i < kNormThreads / 32; ++i) {
-      if (i >= r.warps) break;
-      a.x += p[i].x;
-      if (K > 1) a.y += p[i].y;
-      if (K > 2) a.z += p[i].z;
-    }
-    v[0] = a.x;
-    if (K > 1) v[1] = a.y;
-    if (K > 2) v[2] = a.z;
-  }
-  if (r.C > 1) {
-    const int rank = blockIdx.x % r.C;
-    if ((int)threadIdx.x < r.C) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        uint32_t a;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(a)
-                     : "r"(smem_addr(&r.m->rank_part[b][rank]) + 4 * k), "r"(threadIdx.x));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v[k]) : "memory");
-      }
-    }
-    cluster_barrier();
-    float4 a = r.m->rank_part[b][0];
-    for (int c = 1; c < r.C; ++c) {
-      const float4 z = r.m->rank_part[b][c];
-      a.x += z.x, a.y += z.y, a.z += z.z;
-    }
-    v[0] = a.x;
-    if (K > 1) v[1] = a.y;
-    if (K > 2) v[2] = a.z;
-  }
-  r.turn = b ^ 1;
-}
-
 // ------------------------------------------------------------------- host
 struct NormPlan {
   int C, nt, block, grid;

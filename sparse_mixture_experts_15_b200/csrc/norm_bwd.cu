@@ -70,7 +70,7 @@ __device__ __forceinline__ void row_sums(RowSum6& r, float* v) {
   const int b = r.turn;
   if (r.warps > 1) {
     if ((lane & 3) == 0) r.m->warp_part[b][threadIdx.x >> 5][lane >> 2] = a;
-    asm volatile("bar.sync %0, %1;" ::"r"(r.team + 1), "r"(r.nt) : "memory");
+    team_sync(r.team, r.nt);
     const float* p = &r.m->warp_part[b][r.team * r.warps][lane & 7];
     const int w = lane >> 3;
     a = (w < r.warps ? p[8 * w] : 0.0f) + (w + 4 < r.warps ? p[8 * (w + 4)] : 0.0f);

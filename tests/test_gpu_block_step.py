@@ -228,3 +228,50 @@ def test_training_step():
     assert torch.equal(idx2, fwd["top_idx"])
     moe.moe_route_select_bwd(s, moe.gating(), z, idx2, da, dz)
     assert float((dz - lg["dz"]).norm() / lg["dz"].norm()) <= 1e-2
+
+
+def test_two_steps_at_once():
+    """Two steps on two streams at the same time, each with its own buffers,
+    give what they give alone; tensors made on another stream are used after it."""
+    steps = [ServingStep(300, 512, 16, 4, 128, 4, 1), ServingStep(2, 512, 64, 8, 128, 8, 2)]
+    alone = []
+    for step in steps:
+        step()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in (step.idx, step.w, step.x_out, step.u_next)])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for st, step in zip(streams, steps):
+            with torch.cuda.stream(st):
+                step()
+    torch.cuda.synchronize()
+    for step, ref in zip(steps, alone):
+        got = (step.idx, step.w, step.x_out, step.u_next)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_a_stream_given_by_its_handle():
+    """A call on a stream that is not the current one, its workspace made by the
+    call: the workspace's memory is not given to the next tensor meanwhile."""
+    T, d = 2000, 1024
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, y, dxo, du = (randn(g, T, d).bfloat16() for _ in range(4))
+    w = 1 + randn(g, d, sd=0.1)
+    b = moe.block_norm(T, d, eps=EPS)
+
+    def grads(stream=None):
+        out = dict(dx=torch.empty_like(x), dy=torch.empty_like(x),
+                   dw_post=torch.empty(d, device="cuda"), dw_pre=torch.empty(d, device="cuda"))
+        torch.cuda.synchronize()
+        moe.moe_block_norm_bwd(b, dxo, out, x_out=x, y=y, w_post=w, w_pre=w, du=du,
+                               stream=None if stream is None else stream.cuda_stream)
+        junk = [torch.full((1 << 22,), 7.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        del junk
+        return out
+    ref = grads()
+    for _ in range(5):
+        got = grads(torch.cuda.Stream())
+        assert all(torch.equal(ref[k], got[k]) for k in ref)
