@@ -577,6 +577,7 @@ class _Types:
         self.code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         return self.__dict__[name]
 
 
@@ -606,20 +607,20 @@ def _device(what, t, n, dtypes):
     dev = t.get_device()
     _addr(what, t, n, dtypes, dev)
     if dev < 0:
-        _ptr(t)
+        _ptr(t)  # refuses a host tensor
     return dev
 
 
-def _run(where, dev, stream, *args):
-    """The C call on device dev and its current stream unless one is given."""
+def _run(fn, dev, stream, *args):
+    """The C call fn on device dev and its current stream unless one is given."""
     stream = _t.raw_stream(dev) if stream is None else int(stream)
-    if _t.torch.cuda.current_device() == dev:
-        rc = getattr(_lib, where)(*args, stream)
+    if _t.current_device() == dev:
+        rc = fn(*args, stream)
     else:
         with _t.torch.cuda.device(dev):
-            rc = getattr(_lib, where)(*args, stream)
+            rc = fn(*args, stream)
     if rc != 0:
-        raise MoeError(rc, where)
+        raise MoeError(rc, fn.__name__)
 
 
 def _workspace(ws, dev, stream, query, *args):
@@ -647,7 +648,7 @@ def moe_route_select(s: MoeShape, g: MoeGating, logits, top_idx, top_w, bias=Non
     T, N = s.T, s.N
     TN, Tk, f32 = T * N, T * s.k, _t.f32
     dev = _device("logits", logits, TN, f32)
-    _run("moe_route_select", dev, stream, ctypes.byref(s), ctypes.byref(g), logits.data_ptr(),
+    _run(_lib.moe_route_select, dev, stream, ctypes.byref(s), ctypes.byref(g), logits.data_ptr(),
          _addr("bias", bias, N, f32, dev), _addr("top_idx", top_idx, Tk, _t.i32, dev),
          _addr("top_w", top_w, Tk, f32, dev), _addr("scores", scores, TN, f32, dev))
 
@@ -663,7 +664,7 @@ def moe_route_scored(s: MoeShape, g: MoeGating, u, w_route, top_idx, top_w, bias
             _addr("logits", logits, TN, f32, dev))
     p, n, keep = (None, 0, None) if logits is not None else _workspace(
         ws, dev, stream, _lib.moe_route_scored_workspace_bytes, ctypes.byref(s))
-    _run("moe_route_scored", dev, stream, ctypes.byref(s), ctypes.byref(g), *args, p, n)
+    _run(_lib.moe_route_scored, dev, stream, ctypes.byref(s), ctypes.byref(g), *args, p, n)
 
 
 def moe_route_select_bwd(s: MoeShape, g: MoeGating, logits, top_idx, d_top_w, dz, d_scores=None,
@@ -671,7 +672,7 @@ def moe_route_select_bwd(s: MoeShape, g: MoeGating, logits, top_idx, d_top_w, dz
     """Gradient of the weights (and scores) to the router logits."""
     TN, Tk, f32 = s.T * s.N, s.T * s.k, _t.f32
     dev = _device("logits", logits, TN, f32)
-    _run("moe_route_select_bwd", dev, stream, ctypes.byref(s), ctypes.byref(g), logits.data_ptr(),
+    _run(_lib.moe_route_select_bwd, dev, stream, ctypes.byref(s), ctypes.byref(g), logits.data_ptr(),
          _addr("top_idx", top_idx, Tk, _t.i32, dev), _addr("d_top_w", d_top_w, Tk, f32, dev),
          _addr("d_scores", d_scores, TN, f32, dev), _addr("dz", dz, TN, f32, dev))
 
@@ -691,7 +692,7 @@ def moe_block_norm_fwd(b: MoeBlockNorm, x, y=None, w_post=None, gate=None, w_pre
     n = b.T * d
     dev = _device("x", x, n, _t.act)
     dt = (x.dtype,)
-    _run("moe_block_norm_fwd", dev, stream, ctypes.byref(b), _t.code[x.dtype], x.data_ptr(),
+    _run(_lib.moe_block_norm_fwd, dev, stream, ctypes.byref(b), _t.code[x.dtype], x.data_ptr(),
          _addr("y", y, n, dt, dev), _addr("w_post", w_post, d, f32, dev),
          _gate(b, "gate", gate, dt, dev), _addr("w_pre", w_pre, d, f32, dev),
          _addr("x_out", x_out, n, dt, dev), _addr("u", u, n, dt, dev))
@@ -720,7 +721,7 @@ def moe_block_norm_bwd(b: MoeBlockNorm, dx_out, grads: dict, x_out=None, y=None,
             _addr("w_pre", w_pre, d, f32, dev), _addr("dx_out", dx_out, n, gt, dev),
             _addr("du", du, n, gt, dev))
     p, nb, keep = _workspace(ws, dev, stream, _lib.moe_block_norm_bwd_workspace_bytes, ctypes.byref(b))
-    _run("moe_block_norm_bwd", dev, stream, ctypes.byref(b), _t.code[like.dtype],
+    _run(_lib.moe_block_norm_bwd, dev, stream, ctypes.byref(b), _t.code[like.dtype],
          _t.code[dx.dtype], *args, ctypes.byref(G), p, nb)
 
 
@@ -728,7 +729,7 @@ def moe_quantize_i8_rows(x, codes, scales, stream=None):
     """8-bit integer codes and per-row fp32 scales of x [rows][cols]."""
     rows, cols = x.shape
     dev = _device("x", x, 0, _t.act)
-    _run("moe_quantize_i8_rows", dev, stream, rows, cols, x.data_ptr(), _t.code[x.dtype],
+    _run(_lib.moe_quantize_i8_rows, dev, stream, rows, cols, x.data_ptr(), _t.code[x.dtype],
          _addr("codes", codes, rows * cols, _t.i8, dev), _addr("scales", scales, rows, _t.f32, dev))
 
 
@@ -750,7 +751,7 @@ def moe_grouped_gemm_i8(x, x_scale, w, w_scale, y, offsets=None, ws=None, stream
             _addr("w_scale", w_scale, G * n, f32, dev), _addr("y", y, rows * n, _t.act, dev),
             _t.code[y.dtype])
     p, nb, keep = _workspace(ws, dev, stream, _lib.moe_grouped_gemm_i8_workspace_bytes, rows, G, K, n)
-    _run("moe_grouped_gemm_i8", dev, stream, rows, G, K, n, *args, p, nb)
+    _run(_lib.moe_grouped_gemm_i8, dev, stream, rows, G, K, n, *args, p, nb)
 
 
 def moe_expert_ffn_i8_workspace_bytes(s: MoeShape) -> int:
@@ -774,7 +775,7 @@ def moe_expert_ffn_i8(s: MoeShape, width: int, x_rows, x_scale, offsets, w_gate,
                     _addr("down_scale", down_scale, s.N * width, f32, dev))
     y = _addr("y_rows", y_rows, rows * width, f32, dev)
     p, nb, keep = _workspace(ws, dev, stream, _lib.moe_expert_ffn_i8_workspace_bytes, ctypes.byref(s))
-    _run("moe_expert_ffn_i8", dev, stream, ctypes.byref(s), width, *args, ctypes.byref(S),
+    _run(_lib.moe_expert_ffn_i8, dev, stream, ctypes.byref(s), width, *args, ctypes.byref(S),
          ctypes.byref(a), y, p, nb)
 
 
