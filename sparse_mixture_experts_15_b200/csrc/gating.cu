@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(32 * kSelWarps, PER >= 24 ? 7 : 1)
     route_select(const __grid_constant__ SelectParams p) {
   using L = Lanes<PER>;
   extern __shared__ __align__(16) float sel_mem[];  // per warp: scores, orders [N up to 4]
-  __shared__ uint2 listed[kSelWarps][32];           // (order, expert)
+  // (order, inverted expert) as one number: larger is better
+  __shared__ unsigned long long listed[kSelWarps][32];
   pdl_wait();
   pdl_allow_next();
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, N = p.N;
@@ -275,10 +276,21 @@ __global__ void __launch_bounds__(32 * kSelWarps, PER >= 24 ? 7 : 1)
       rank += o > mine || (o == mine && h < g);
     }
     const uint32_t kept = __ballot_sync(0xffffffffu, g < G && rank < p.top_group);
+    // bit h << sub_log of kept is group h's (an expert past N has the order 0 anyway)
+    if (L::CH == 4 && p.per % 4 == 0) {  // a chunk is of one group
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const uint32_t h = L::expert(lane, e) * p.inv >> 20;
-      if (h < (uint32_t)G && !((kept >> (h << p.sub_log)) & 1u)) ord[e] = 0u;
+      for (int e = 0; e < PER; e += 4) {
+        const uint32_t h = L::expert(lane, e) * p.inv >> 20;
+        const uint32_t all = (kept >> ((h << p.sub_log) & 31u)) & 1u ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ord[e + i] &= all;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const uint32_t h = L::expert(lane, e) * p.inv >> 20;
+        if (!((kept >> ((h << p.sub_log) & 31u)) & 1u)) ord[e] = 0u;
+      }
     }
   }
   uint32_t best = 0u;
@@ -306,18 +318,15 @@ __global__ void __launch_bounds__(32 * kSelWarps, PER >= 24 ? 7 : 1)
     at -= own;
     while (in) {
       const int j = L::expert(lane, __ffs(in) - 1);
-      listed[wib][at++] = make_uint2(od[j], j);
+      listed[wib][at++] = (unsigned long long)od[j] << 32 | (uint32_t)~j;
       in &= in - 1;
     }
     __syncwarp();
-    const uint2 c = lane < count ? listed[wib][lane] : make_uint2(0u, 0u);
+    const unsigned long long c = lane < count ? listed[wib][lane] : 0u;
     int ahead = 0;
 #pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-      const uint2 o = listed[wib][i];
-      ahead += o.x > c.x || (o.x == c.x && o.y < c.y);
-    }
-    mine = c.y;
+    for (int i = 0; i < count; ++i) ahead += listed[wib][i] > c;
+    mine = (int)~(uint32_t)c;
     if (lane < count) slot = ahead;
   } else {
     int first = 0;  // this lane's best
