@@ -36,6 +36,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "pairs.cuh"
 #include "tc_primitives.cuh"
 
 namespace moe {
@@ -100,6 +101,30 @@ struct TcParams {
 
 __device__ __forceinline__ void named_sync_epi() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+__device__ __forceinline__ void scale2(float* v, Pair f) {
+  const float2 r = parts(mul2(pair(v[0], v[1]), f));
+  v[0] = r.x;
+  v[1] = r.y;
+}
+
+// An output column's values of 32 tokens, of which n are stored.  All of them
+// without a test of each: with one, and an address of its own by 64-bit steps,
+// the stores were 21 instructions a value and bound tiles of few k-blocks.
+template <typename O>
+__device__ __forceinline__ void store_tokens(O* out, int ld, int n, const float* v) {
+  char* o = reinterpret_cast<char*>(out);
+  const size_t step = (size_t)ld * sizeof(O);
+  if (n >= 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      *reinterpret_cast<O*>(o + step * j) = from_f32<O>(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) *reinterpret_cast<O*>(o + step * j) = from_f32<O>(v[j]);
+  }
 }
 
 template <int BN, int S, int CG = 1>
@@ -479,9 +504,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(__float_as_int(v[j]));
         }
-        if (F8 || I8 || p.b_scale) {  // row scales of A and of B (codes, or combine weights)
+        // row scales of A (codes) and of B (codes, or combine weights)
+        if (F8 || I8) {
+          const Pair w2 = pair(w_scale, w_scale);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = v[j] * w_scale * (p.b_scale ? fac[c + j] : 1.0f);
+          for (int j = 0; j < 32; j += 2) scale2(v + j, w2);
+        }
+        if (p.b_scale) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + c + j);
+            scale2(v + j, f.x);
+            scale2(v + j + 2, f.y);
+          }
         }
         if (p.mode == MODE_GATEUP) {
 #pragma unroll
@@ -521,24 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
           // 8-bit integers take any number of output columns: the last tile
           // may pass them, its extra weight rows are another group's or zeros
           const int stored = !I8 || a < p.a_rows_per_group ? n_valid : 0;
-          if (I8 && p.mode == MODE_STORE_F16) {
-            __half* o = static_cast<__half*>(p.out);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < stored)
-                o[(size_t)(tok0 + c + j) * p.out_ld + col] = __float2half_rn(v[j]);
-          } else if (p.mode == MODE_STORE_F32) {
-            float* o = static_cast<float*>(p.out);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < stored) o[(size_t)(tok0 + c + j) * p.out_ld + col] = v[j];
-          } else {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < stored)
-                o[(size_t)(tok0 + c + j) * p.out_ld + col] = __float2bfloat16_rn(v[j]);
-          }
+          const size_t at = (size_t)(tok0 + c) * p.out_ld + col;
+          if (I8 && p.mode == MODE_STORE_F16)
+            store_tokens(static_cast<__half*>(p.out) + at, p.out_ld, stored - c, v);
+          else if (p.mode == MODE_STORE_F32)
+            store_tokens(static_cast<float*>(p.out) + at, p.out_ld, stored - c, v);
+          else
+            store_tokens(static_cast<__nv_bfloat16*>(p.out) + at, p.out_ld, stored - c, v);
         }
       }
       tc::tc_fence_before();
