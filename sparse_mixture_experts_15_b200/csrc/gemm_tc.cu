@@ -18,7 +18,7 @@
 // Persistent kernel, one CTA per SM, 6 warps:
 //   warp 0    TMA producer (one elected lane), S-stage smem ring
 //   warp 1    TMEM allocator + single-thread tcgen05.mma issuer
-//   warps 2-5 epilogue: tcgen05.ld TMEM -> registers -> global
+//   warps 2-5 epilogue: tcgen05.ld TMEM -> registers -> global (8-bit integers: 2-9)
 // Two TMEM accumulators (2 x BN columns) let the epilogue of tile i overlap
 // the MMAs of tile i+1.  Every mbarrier wait is bounded; a wait that runs out
 // records MOE_ERR_TIMEOUT, stops all roles, drains in-flight TMA loads and
@@ -60,7 +60,6 @@ namespace {
 
 constexpr int kBM = 128;
 constexpr int kBK = 64;  // 64 bf16 = 128 bytes = one swizzle span (128 E4M3 codes)
-constexpr int kThreads = 192;
 constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s)
 constexpr int kEpiLd = 33;                       // padded row of the gate/up exchange tile
 
@@ -99,8 +98,14 @@ struct TcParams {
   const float* b_scale;
 };
 
-__device__ __forceinline__ void named_sync_epi() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+// Teams of four epilogue warps, one warp for each quarter of TMEM's lanes.  The
+// stores of 8-bit products take two, which share out a tile's columns: their
+// tiles of few k-blocks are bound by the epilogue's instructions, and one warp
+// per scheduler issues one in two and a half cycles.
+constexpr int epi_teams(int kind) { return kind == OPS_I8 ? 2 : 1; }
+constexpr int tc_threads(int kind) { return 64 + 128 * epi_teams(kind); }
+__device__ __forceinline__ void named_sync_epi(int team) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
 }
 
 __device__ __forceinline__ void scale2(float* v, Pair f) {
@@ -127,12 +132,13 @@ __device__ __forceinline__ void store_tokens(O* out, int ld, int n, const float*
   }
 }
 
-template <int BN, int S, int CG = 1>
+template <int BN, int S, int CG, int KIND>
 struct Layout {
   static constexpr int A_BYTES = kBM * kBK * 2;
   static constexpr int B_BYTES = BN / CG * kBK * 2;  // this CTA's token rows
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int EPI_BYTES = kBM * kEpiLd * 4 + BN * 4;  // exchange tile + token factors
+  static constexpr int EPI_BYTES =  // exchange tile, and the teams' token factors
+      kBM * kEpiLd * 4 + epi_teams(KIND) * BN * 4;
   static size_t bytes(int G) {
     size_t b = 1024;  // alignment slack of the dynamic smem base
     b += (size_t)S * STAGE + EPI_BYTES;
@@ -152,8 +158,9 @@ struct Layout {
 //             scales applied to the sums' fp32 values; gate/up mode stores H
 //             as bf16
 template <int BN, int S, int ACT, int CG, int KIND>
-__global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_constant__ TcParams p) {
-  using L = Layout<BN, S, CG>;
+__global__ void __launch_bounds__(tc_threads(KIND), 1)
+    tc_grouped_gemm(const __grid_constant__ TcParams p) {
+  using L = Layout<BN, S, CG, KIND>;
   constexpr bool F8 = KIND == OPS_E4M3, I8 = KIND == OPS_I8;
   constexpr int KE = F8 || I8 ? 2 * kBK : kBK;  // elements per 128-byte k-block
   static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair per MMA");
@@ -167,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* stages = smem;
   float* epi = reinterpret_cast<float*>(smem + S * L::STAGE);
-  float* fac = epi + kBM * kEpiLd;  // [BN] the tile's token-row factors (b_scale)
-  int* grp_beg = reinterpret_cast<int*>(fac + BN);
+  float* facs = epi + kBM * kEpiLd;  // [teams][BN] the tile's token-row factors (b_scale)
+  int* grp_beg = reinterpret_cast<int*>(facs + epi_teams(KIND) * BN);
   int* grp_cnt = grp_beg + (p.G + 1);
   int* grp_pre = grp_cnt + (p.G + 1);
   uint64_t* bars = reinterpret_cast<uint64_t*>(
@@ -194,9 +201,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(tc::smem_u32(&tfull[b]), 1);
-      // one CTA: every epilogue thread arrives; a pair: one thread per CTA
-      // arrives on the even CTA's barrier
-      tc::mbar_init(tc::smem_u32(&tempty[b]), CG == 2 ? 2 : 128);
+      // one CTA: every epilogue thread arrives; a pair: one thread per team
+      // and CTA arrives on the even CTA's barrier
+      tc::mbar_init(tc::smem_u32(&tempty[b]), (CG == 2 ? 2 : 128) * epi_teams(KIND));
     }
     tc::mbar_init(tc::smem_u32(drain), 1);
     tc::fence_barrier_init();
@@ -431,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const int row = q * 32 + lane;
+    const int team = epi_teams(KIND) == 1 ? 0 : (warp - 2) >> 2;
+    float* fac = facs + team * BN;
+    // gate/up tiles are exchanged in one buffer, by the first team
+    const int teams = fused ? 1 : epi_teams(KIND);
     // A tile's token-row factors (thread `row` has columns row, row + 128) and
     // this thread's weight-row scale, loaded one tile ahead: a tile of few
     // k-blocks is over before such a load is.
@@ -471,24 +482,24 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
       // the factors go to shared memory once every epilogue warp is done with
       // the previous tile's
       if (p.b_scale) {
-        named_sync_epi();
+        named_sync_epi(team);
 #pragma unroll
         for (int i = 0; i < NF; ++i)
           if (row + 128 * i < BN) fac[row + 128 * i] = next_fac[i];
       }
       const float w_scale = next_scale;
       prefetch(tile + n_units);
-      // The four epilogue warps share named barriers, so they take the
+      // The four warps of a team share a named barrier, so they take the
       // give-up decision together (the barrier also publishes fac).
       const bool got = tc::mbar_wait(tc::smem_u32(&tfull[b]), use & 1u, abort_flag, kWaitBudget);
       uint32_t all_ok;
       asm volatile(
           "{\n\t.reg .pred p, q;\n\t"
           "setp.ne.u32 p, %1, 0;\n\t"
-          "bar.red.and.pred q, 1, 128, p;\n\t"
+          "bar.red.and.pred q, %2, 128, p;\n\t"
           "selp.u32 %0, 1, 0, q;\n\t}"
           : "=r"(all_ok)
-          : "r"((uint32_t)got)
+          : "r"((uint32_t)got), "r"(1 + team)
           : "memory");
       if (!all_ok) {
         record_error(p.status, MOE_ERR_TIMEOUT);
@@ -497,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
       }
       tc::tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
-      for (int c = 0; c < n_valid; c += 32) {
+      for (int c = team < teams ? 32 * team : n_valid; c < n_valid; c += 32 * teams) {
         float v[32];
         tc::tmem_ld_32x32b_x32(t_row + (uint32_t)c, v);
         if (I8) {
@@ -521,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
         if (p.mode == MODE_GATEUP) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) epi[row * kEpiLd + j] = v[j];
-          named_sync_epi();
+          named_sync_epi(team);
           const int tok = c + lane;
           if (tok < n_valid) {
             float hv[16];
@@ -549,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
               o[1] = make_uint4(packed[4], packed[5], packed[6], packed[7]);
             }
           }
-          named_sync_epi();
+          named_sync_epi(team);
         } else {
           const int a = (m * CG + (int)rank) * kBM + row;
           const int col = g * p.out_col_group + a;
@@ -567,9 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_grouped_gemm(const __grid_cons
       }
       tc::tc_fence_before();
       if (CG == 2) {
-        // this CTA's 128 lanes are read: one arrival on the even CTA's barrier
-        named_sync_epi();
-        if (threadIdx.x == 64) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[b]), 0u));
+        // the team has read its part: one arrival on the even CTA's barrier
+        named_sync_epi(team);
+        if (threadIdx.x == 64 + 128 * team)
+          tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[b]), 0u));
       } else {
         tc::mbar_arrive(tc::smem_u32(&tempty[b]));
       }
@@ -633,13 +645,13 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, u
 // device: a persistent pair kernel launches exactly that many, never more,
 // so that no cluster waits for another to finish.
 template <typename Kernel>
-int resident_pairs(Kernel kernel, size_t smem, int dev) {
+int resident_pairs(Kernel kernel, int threads, size_t smem, int dev) {
   static std::atomic<int> cached[kMaxDevices];
   int n = cached[dev].load(std::memory_order_relaxed);
   if (n) return n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)sm_count());
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -658,7 +670,7 @@ int resident_pairs(Kernel kernel, size_t smem, int dev) {
 
 template <int BN, int S, int ACT, int CG, int KIND>
 int launch_tc(const TcParams& p, int64_t units_upper, cudaStream_t st) {
-  using L = Layout<BN, S, CG>;
+  using L = Layout<BN, S, CG, KIND>;
   auto kernel = tc_grouped_gemm<BN, S, ACT, CG, KIND>;
   const size_t smem = L::bytes(p.G);
   static std::atomic<bool> configured[kMaxDevices];
@@ -676,15 +688,15 @@ int launch_tc(const TcParams& p, int64_t units_upper, cudaStream_t st) {
   if (CG == 1) {
     int64_t grid = sm_count();
     if (units_upper < grid) grid = units_upper;
-    launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, p);
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(tc_threads(KIND)), smem, st, p);
     return launch_status();
   }
-  int64_t pairs = resident_pairs(kernel, L::bytes(1024), dev);
+  int64_t pairs = resident_pairs(kernel, tc_threads(KIND), L::bytes(1024), dev);
   if (pairs <= 0) return MOE_ERR_CUDA;
   if (units_upper < pairs) pairs = units_upper;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(tc_threads(KIND));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -721,6 +733,26 @@ int pick_bn_i8(int m_tiles, int64_t max_rows, int G, int cg) {
   if (max_rows <= 8LL * G) return 32;
   if (max_rows <= 32LL * G) return 64;
   return pick_bn(m_tiles, max_rows, G, cg);
+}
+
+// Tiles of a plain 8-bit product.  Groups of few rows take single CTAs, whose
+// finer tiles fill the SMs more evenly (64 groups of 24 rows, 1040 -> 2056: 42.7
+// -> 38.4 us), and so do products whose 128 x 128 tiles are one round over the
+// SMs (441 rows 736 -> 1304: 6.1 us, 256 wide on pairs 9.0; 3456 rows in 8 groups
+// 656 -> 512: 7.0 and 8.5) and those of at most four k-blocks, which the stores
+// bound (7608 rows in 8 groups 432 -> 2200: 24.6 and 26.7; 2227 in 64 368 ->
+// 4752: 39.8, 128 wide on pairs 56.5).  Pairs elsewhere, 256 wide where groups
+// average 192 rows (2876 in 8 2496 -> 4808: 37.4, 128 wide 46.8, single CTAs
+// 42.7; 1255 in 2 2080 -> 1848: 12.2, 14.8, 12.7).
+struct TileI8 {
+  int bn, cg;
+};
+TileI8 pick_tile_i8(int m_rows, int kblocks, int64_t max_rows, int G) {
+  const int m128 = (m_rows + kBM - 1) / kBM;
+  if (max_rows <= 32LL * G) return {pick_bn_i8(m128, max_rows, G, 1), 1};
+  const bool one_round = m128 * ((max_rows + 127) / 128 + G) <= sm_count();
+  const int bn = one_round || max_rows < 192LL * G ? 128 : 256;
+  return {bn, m_rows <= kBM || one_round || kblocks <= 4 ? 1 : 2};
 }
 
 template <int KIND>
@@ -841,14 +873,11 @@ int tc_store(const int32_t* offsets, int T, int G, int m_rows, const TcSeg* segs
   TcParams p{};
   const int64_t max_rows = offsets ? segs[0].b_rows : (int64_t)T * G;
   // CTA pairs take 256 output rows (128 per CTA) per tile; for 8-bit integers
-  // the last tile may be ragged (and the last k-block: the loads fill zeros),
-  // and groups of few rows take single CTAs, whose finer tiles fill the SMs more
-  // evenly (64 groups of 24 rows, 1040 -> 2056: 42.7 -> 38.4 us)
-  const int cg = i8 ? (m_rows > kBM && max_rows > 32LL * G ? 2 : 1)
-                 : m_rows % (2 * kBM) == 0 ? 2 : 1;
+  // the last tile may be ragged (and the last k-block: the loads fill zeros)
+  const TileI8 t8 = i8 ? pick_tile_i8(m_rows, (segs[0].K + ke - 1) / ke, max_rows, G) : TileI8{};
+  const int cg = i8 ? t8.cg : m_rows % (2 * kBM) == 0 ? 2 : 1;
   const int m_tiles = (m_rows + kBM * cg - 1) / (kBM * cg);
-  const int bn = kind == OPS_I8 ? pick_bn_i8(m_tiles, max_rows, G, cg)
-                                : pick_bn(m_tiles, max_rows, G, cg);
+  const int bn = i8 ? t8.bn : pick_bn(m_tiles, max_rows, G, cg);
   // distinct (pointer, rows, cols, box) tensor maps, at most four
   const void* key_p[4];
   int64_t key_r[4];
