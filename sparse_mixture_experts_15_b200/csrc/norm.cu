@@ -9,9 +9,8 @@
 namespace moe {
 namespace {
 
-// CTAs per SM (three, of 80 registers a thread, spill and take 59 us where two
-// take 45: 8192 x 4096 bf16, both norms)
-constexpr int kFwdCtas = 2;
+// Threads of an SM: 512 (768, of 80 registers each, spill and take 59 us where
+// 512 take 45: 8192 x 4096 bf16, both norms).
 
 struct NormFwd {
   int T, d, C;             // C: CTAs of a cluster, each with its share of a row's columns
@@ -28,49 +27,48 @@ struct NormFwd {
 // distributed shared memory.  Two buffers taken in turn: a thread writes a buffer
 // again only after a barrier that every reader of its last contents has reached.
 struct RowSumMem {
-  float warp_part[2][kNormThreads / 32];  // by warp of the CTA
+  float warp_part[2][kWideThreads / 32];  // by warp of the CTA
   float rank_part[2][4];
+  uint64_t bar[2];
 };
 struct RowSum {
   RowSumMem* m;
   int team, nt, warps, C;  // warps: of this team
-  int turn;
+  uint32_t uses;
+  Exchange cluster;
 };
+template <int THREADS>
 __device__ __forceinline__ float row_sum(RowSum& r, float v) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int b = r.turn;
+  const int b = r.uses & 1;
   if (r.warps > 1) {
     if ((threadIdx.x & 31) == 0) r.m->warp_part[b][threadIdx.x >> 5] = v;
     team_sync(r.team, r.nt);
     const float* p = &r.m->warp_part[b][r.team * r.warps];
     v = p[0];
 #pragma unroll
-    for (int i = 1; i < kNormThreads / 32; ++i) {
+    for (int i = 1; i < THREADS / 32; ++i) {
       if (i >= r.warps) break;
       v += p[i];
     }
   }
   if (r.C > 1) {  // warps > 1: rows this wide fill their teams
-    if ((int)threadIdx.x < r.C) {
-      uint32_t a;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(a)
-                   : "r"(smem_addr(&r.m->rank_part[b][blockIdx.x % r.C])), "r"(threadIdx.x));
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-    }
-    cluster_barrier();
+    if (threadIdx.x == 0) r.cluster.expect(b, 4 * r.C);
+    if ((int)threadIdx.x < r.C)
+      r.cluster.send(b, &r.m->rank_part[b][blockIdx.x % r.C], threadIdx.x, v);
+    r.cluster.wait(b, (r.uses >> 1) & 1);
     v = r.m->rank_part[b][0];
     for (int c = 1; c < r.C; ++c) v += r.m->rank_part[b][c];
   }
-  r.turn = b ^ 1;
+  ++r.uses;
   return v;
 }
 
 // HASY: a block's output comes in (POST: normed first; FULL: gated by element;
 // a channel's gate is part of coef, a token's of the row's factor).
-template <typename T, int S, bool HASY, bool POST, bool FULL, bool PRE>
-__global__ void __launch_bounds__(kNormThreads, kFwdCtas)
+template <typename T, int THREADS, int S, bool HASY, bool POST, bool FULL, bool PRE>
+__global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
     block_norm_fwd(const __grid_constant__ NormFwd p) {
   extern __shared__ __align__(128) char ring_mem[];
   __shared__ RowSumMem sum_mem;
@@ -78,7 +76,8 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
   constexpr int W = chunk_width<T, T>(), NV = kCols / W, E = sizeof(T), A = 1 + HASY + FULL;
   const int nt = p.nt;
   const Place q = place_of(nt, p.C, p.d, p.T);
-  RowSum sums{&sum_mem, q.team, nt, nt / 32, p.C, 0};
+  RowSum sums{&sum_mem, q.team, nt, nt / 32, p.C, 0, {smem_addr(sum_mem.bar), true, p.status}};
+  if (p.C > 1) sums.cluster.init();
   const uint32_t slot = nt * kCols * E;  // bytes of an array in a stage
   const uint32_t ring = smem_addr(ring_mem) + q.team * S * A * slot;
   const uint32_t bar = smem_addr(full_bar[q.team]);
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
         Pair a = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) a = fma2(y[k], y[k], a);
-        r *= rsqrtf(fmaf(row_sum(sums, sum2(a)), p.inv_d, p.eps));
+        r *= rsqrtf(fmaf(row_sum<THREADS>(sums, sum2(a)), p.inv_d, p.eps));
       }
       const Pair rr = pair(r, r);
 #pragma unroll
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
       Pair a = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) a = fma2(x[k], x[k], a);
-      const float r1 = rsqrtf(fmaf(row_sum(sums, sum2(a)), p.inv_d, p.eps));
+      const float r1 = rsqrtf(fmaf(row_sum<THREADS>(sums, sum2(a)), p.inv_d, p.eps));
       const Pair rr = pair(r1, r1);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = mul2(mul2(x[k], rr), wpre[k]);
@@ -165,19 +164,25 @@ __global__ void __launch_bounds__(kNormThreads, kFwdCtas)
     at_row.next();
   }
   if (leader) at_row.drain();
+  if (p.C > 1) cluster_barrier();  // no CTA leaves while another may write to it
 }
 
-// Stages of the ring: as many as leave room for two CTAs per SM, 2 to 4.
-template <typename T, bool HASY, bool POST, bool FULL, bool PRE>
-int run_fwd(const NormFwd& p0, cudaStream_t st) {
+// Stages of the ring: as many as leave room for an SM's threads, 2 to 4.
+template <typename T, int THREADS, bool HASY, bool POST, bool FULL, bool PRE>
+int run_threads(const NormFwd& p0, cudaStream_t st) {
   static std::atomic<bool> configured[kMaxDevices];
   constexpr int row = kCols * (int)sizeof(T) * (1 + HASY + FULL);
-  constexpr int fit = kNormSmem / (row * kNormThreads * kFwdCtas), S = fit > 4 ? 4 : fit;
+  constexpr int fit = kNormSmem / (row * kSmThreads), S = fit > 4 ? 4 : fit;
   NormFwd p = p0;
-  const NormPlan q = norm_plan(p.T, p.d, S * row, kFwdCtas);
+  const NormPlan q = norm_plan(p.T, p.d, S * row, THREADS);
   p.C = q.C;
   p.nt = q.nt;
-  return launch_norm(block_norm_fwd<T, S, HASY, POST, FULL, PRE>, configured, p, q, st);
+  return launch_norm(block_norm_fwd<T, THREADS, S, HASY, POST, FULL, PRE>, configured, p, q, st);
+}
+template <typename T, bool HASY, bool POST, bool FULL, bool PRE>
+int run_fwd(const NormFwd& p, cudaStream_t st) {
+  return norm_wide(p.T, p.d, 4096) ? run_threads<T, kWideThreads, HASY, POST, FULL, PRE>(p, st)
+                             : run_threads<T, kNormThreads, HASY, POST, FULL, PRE>(p, st);
 }
 
 template <typename T>

@@ -1,6 +1,6 @@
 // Pieces of the block-norm kernels (norm.cu, norm_bwd.cu).
 //
-// A team of nt threads (a multiple of 32, at most 256) takes a row, 16 columns a
+// A team of nt threads (a multiple of 32, at most 512) takes a row, 16 columns a
 // thread, so that the fixed work of a row (its sums' shuffles, the barriers, the
 // addresses) is spread over many columns; teams walk the rows with a stride.
 // One thread of a team starts bulk copies of the next rows into a ring in
@@ -8,9 +8,10 @@
 // instructions of the other threads.  (Copies by every thread, cp.async, reached
 // the same bandwidth alone, but not next to the row's arithmetic: 136 us against
 // 106 for the gradients of 8192 x 4096 bf16 with fp32 stream gradients.)
-// Arithmetic is on pairs (one instruction for two fp32 operations).  Rows
-// above 4096 columns go to a cluster of two or four CTAs that exchange their sums
-// through distributed shared memory.
+// Arithmetic is on pairs (one instruction for two fp32 operations).  Two CTAs
+// of 256 threads share an SM for rows of up to 4096 columns; wider rows take
+// CTAs of 512 (norm_wide), and where that isn't enough a cluster of two, whose
+// sums go through distributed shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -19,8 +20,9 @@
 
 namespace moe {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormMaxD = 16384;       // a cluster of 4 CTAs of 256 threads x 16 columns
+constexpr int kNormThreads = 256, kWideThreads = 512;
+constexpr int kSmThreads = 512;        // of an SM: what 128 registers a thread leave room for
+constexpr int kNormMaxD = 16384;       // a cluster of 2 CTAs of 512 threads x 16 columns
 constexpr int kNormSmem = 200 * 1024;  // dynamic shared memory of an SM that the CTAs take, at most
 
 namespace {
@@ -150,7 +152,7 @@ __device__ __forceinline__ void gains(const Place& q, int nt, const float* a, co
 // that its first thread starts; a stage's barrier completes when they landed.
 // Columns that the row does not have stay the zeros they are set to here.
 constexpr long long kRowWait = 4000000000LL;  // cycles (~2 s)
-constexpr int kMaxTeams = kNormThreads / 32;
+constexpr int kMaxTeams = kNormThreads / 32;  // (a wide CTA is one team)
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -212,25 +214,90 @@ __device__ __forceinline__ void cluster_barrier() {
                ::: "memory");
 }
 
+// The exchange of a cluster's sums: a CTA's values go to every CTA of the
+// cluster by stores that count on the receiver's barrier, two barriers in turn.
+// (A cluster barrier instead orders the row's stores to global memory first,
+// which takes longer than the sums: 4096 bf16 rows of 16384, both norms, 190 us.)
+// A barrier's next use can't begin early: a CTA sends use k + 2 after it has all
+// of use k + 1, and this CTA's part of that is sent after all its threads are
+// past use k.  A wait that runs out records an error, once, and later ones do
+// not wait; the kernel's closing cluster barrier keeps every receiver alive.
+struct Exchange {
+  uint32_t bar;  // of the two barriers
+  bool ok;
+  int* status;
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      tc::mbar_init(bar, 1);
+      tc::mbar_init(bar + 8, 1);
+      tc::fence_barrier_init();
+    }
+  }
+  // bytes: that come in for this use, the CTA's own among them; one thread
+  __device__ __forceinline__ void expect(int turn, uint32_t bytes) {
+    tc::mbar_arrive_expect_tx(bar + 8 * turn, bytes);
+  }
+  // v to the CTA `to`, where slot is in this one
+  __device__ __forceinline__ void send(int turn, const float* slot, int to, float v) {
+    uint32_t a, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(slot)), "r"(to));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(bar + 8 * turn), "r"(to));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(a),
+                 "r"(__float_as_uint(v)), "r"(b)
+                 : "memory");
+  }
+  __device__ __forceinline__ void wait(int turn, uint32_t phase) {
+    if (!ok) return;
+    const long long t0 = clock64();
+    uint32_t done = 0;
+    while (true) {
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(bar + 8 * turn), "r"(phase)
+          : "memory");
+      if (done) return;
+      if (clock64() - t0 > kRowWait) break;
+    }
+    record_error(status, MOE_ERR_TIMEOUT);
+    ok = false;
+  }
+};
+
 // ------------------------------------------------------------------- host
 struct NormPlan {
   int C, nt, block, grid;
   size_t smem;
 };
 
-// bytes: of the ring per thread.  ctas: CTAs of 256 threads per SM.  Few rows
-// are spread over the SMs before a CTA gets a second team.
-inline NormPlan norm_plan(int T, int d, int bytes, int ctas) {
+// Rows for CTAs of 512 threads: a sum over a CTA costs less than one over a
+// cluster, and 8192 columns need none (4096 bf16 rows of 8192, both norms: 57.7
+// us, clusters of two CTAs of 256 89.3; of 16384, clusters of two 190, of four
+// 323).  Up to 4096 columns two CTAs an SM hide one another's barriers (8192 x
+// 4096: 44.9 us, one of 512 48.0), and above 8192 more, smaller CTAs take a few
+// rows faster (one row of 16384: 3.8 and 5.4 us).
+// above: columns from which they are taken (the gradients: 5120, as clusters of two
+// have three CTAs on an SM up to there, 4096 rows 92.1 us and 96.8; of 6144 117.6
+// and 106.7).
+inline bool norm_wide(int T, int d, int above) {
+  return d > above && (d <= 16 * kWideThreads || T > sm_count() / 2);
+}
+
+// bytes: of the ring per thread.  threads: of a CTA, at most.  Few rows are
+// spread over the SMs before a CTA gets a second team.
+inline NormPlan norm_plan(int T, int d, int bytes, int threads) {
   NormPlan q;
   const int sms = sm_count(), chunks = d / 8;
-  q.C = chunks <= 2 * kNormThreads ? 1 : chunks <= 4 * kNormThreads ? 2 : 4;
+  q.C = chunks <= 2 * threads ? 1 : chunks <= 4 * threads ? 2 : 4;
   q.nt = ((chunks + 2 * q.C - 1) / (2 * q.C) + 31) / 32 * 32;
-  int teams = kNormThreads / q.nt;
+  int teams = threads / q.nt;
   const int spread = (T + sms - 1) / sms;
   if (teams > spread) teams = spread;
   q.block = teams * q.nt;
   q.smem = (size_t)bytes * q.block;
-  int per_sm = kNormThreads * ctas / q.block;
+  int per_sm = kSmThreads / q.block;
   const int fit = (int)(kNormSmem / q.smem);
   if (per_sm > fit) per_sm = fit;
   const int64_t want = (int64_t)((T + teams - 1) / teams) * q.C;

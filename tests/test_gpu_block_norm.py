@@ -244,6 +244,16 @@ def test_backward_many_rows(T, d, gate):
     check_backward(inputs(T, d, torch.bfloat16, gate, True, True, 4), torch.float32, 5)
 
 
+@pytest.mark.parametrize("T,d", [(301, 4104), (331, 8192), (70, 8200), (230, 16384)])
+def test_wide_rows(T, d):
+    """Rows of one CTA and of a cluster, more and fewer than run at once."""
+    for dtype, grad, gate in (("bf16", "bf16", "full"), ("bf16", "f32", "token"),
+                              ("f16", "f16", "channel"), ("f32", "f32", "none")):
+        t = inputs(T, d, DT[dtype], gate, True, True, d + T)
+        check_forward(t)
+        check_backward(t, DT[grad], T)
+
+
 def test_backward_without_stream_gradient_or_branch():
     t = inputs(33, 1000, torch.bfloat16, "channel", True, True, 1)
     check_backward(t, torch.float32, 2, dxo_none=True)
