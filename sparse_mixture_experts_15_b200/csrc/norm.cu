@@ -9,8 +9,16 @@
 namespace moe {
 namespace {
 
-// Threads of an SM: 512 (768, of 80 registers each, spill and take 59 us where
-// 512 take 45: 8192 x 4096 bf16, both norms).
+// CTAs per SM (three, of 80 registers a thread, spill and take 59 us where two
+// take 45: 8192 x 4096 bf16, both norms)
+constexpr int kFwdCtas = 2;
+
+// Stages of a team's ring.  More of them let the reads run ahead of the stores,
+// and the memory serves the two worse: 16384 x 4096 bf16, both norms, 83.4 us, with
+// four stages 96.4 (the pre norm alone 82.3 and 90.9; 2048 rows 13.8 and 14.1, the
+// pre norm alone 12.8 and 12.3).  A row's stage is filled again once the first
+// sum's barrier shows that its threads have read it (at the row's end: 86.4).
+constexpr int kFwdStages = 2;
 
 struct NormFwd {
   int T, d, C;             // C: CTAs of a cluster, each with its share of a row's columns
@@ -22,12 +30,14 @@ struct NormFwd {
   int* status;
 };
 
-// A sum over the threads of a row: lanes by a shuffle tree, the team's warps in
-// order from shared memory, then the CTAs of the cluster in rank order through
+// A sum over the threads of a row: lanes by a shuffle tree, the team's warps from
+// shared memory in a fixed order, then the CTAs of the cluster in rank order through
 // distributed shared memory.  Two buffers taken in turn: a thread writes a buffer
 // again only after a barrier that every reader of its last contents has reached.
 struct RowSumMem {
-  float warp_part[2][kWideThreads / 32];  // by warp of the CTA
+  // by team, whose warps' parts are padded with zeros to a multiple of four: at
+  // most four teams of two warps, two of three or four, one of more
+  float4 warp_part[2][4];
   float rank_part[2][4];
   uint64_t bar[2];
 };
@@ -37,20 +47,20 @@ struct RowSum {
   uint32_t uses;
   Exchange cluster;
 };
-template <int THREADS>
 __device__ __forceinline__ float row_sum(RowSum& r, float v) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int b = r.uses & 1;
   if (r.warps > 1) {
-    if ((threadIdx.x & 31) == 0) r.m->warp_part[b][threadIdx.x >> 5] = v;
+    const float4* p = &r.m->warp_part[b][r.team];
+    if ((threadIdx.x & 31) == 0)
+      reinterpret_cast<float*>(r.m->warp_part[b] + r.team)[(threadIdx.x >> 5) - r.team * r.warps] = v;
     team_sync(r.team, r.nt);
-    const float* p = &r.m->warp_part[b][r.team * r.warps];
-    v = p[0];
-#pragma unroll
-    for (int i = 1; i < THREADS / 32; ++i) {
-      if (i >= r.warps) break;
-      v += p[i];
+    const float4 a = p[0];
+    v = (a.x + a.y) + (a.z + a.w);
+    if (r.warps > 4) {
+      const float4 c = p[1];
+      v += (c.x + c.y) + (c.z + c.w);
     }
   }
   if (r.C > 1) {  // warps > 1: rows this wide fill their teams
@@ -67,9 +77,10 @@ __device__ __forceinline__ float row_sum(RowSum& r, float v) {
 
 // HASY: a block's output comes in (POST: normed first; FULL: gated by element;
 // a channel's gate is part of coef, a token's of the row's factor).
-template <typename T, int THREADS, int S, bool HASY, bool POST, bool FULL, bool PRE>
-__global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
+template <typename T, bool HASY, bool POST, bool FULL, bool PRE>
+__global__ void __launch_bounds__(kNormThreads, kFwdCtas)
     block_norm_fwd(const __grid_constant__ NormFwd p) {
+  constexpr int S = kFwdStages;
   extern __shared__ __align__(128) char ring_mem[];
   __shared__ RowSumMem sum_mem;
   __shared__ uint64_t full_bar[kMaxTeams][S];
@@ -82,6 +93,8 @@ __global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
   const uint32_t ring = smem_addr(ring_mem) + q.team * S * A * slot;
   const uint32_t bar = smem_addr(full_bar[q.team]);
   const bool leader = q.lane_t == 0;
+  if (threadIdx.x < 8) sum_mem.warp_part[threadIdx.x >> 2][threadIdx.x & 3] = make_float4(0, 0, 0, 0);
+  __syncthreads();
   if (leader) {
     for (int s = 0; s < S; ++s) tc::mbar_init(bar + 8 * s, 1);
     tc::fence_barrier_init();
@@ -110,6 +123,12 @@ __global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
   const uint32_t mine = q.lane_t * W * E, next = nt * W * E;  // this thread's first chunk, its step
   uint32_t t = q.first;
   Ring at_row{bar, S, 0, 0, true, 0, 0};
+  // the row S on into the stage of row i, which every thread of the team has read:
+  // it has passed a barrier since
+  auto refill = [&](int i, uint32_t t, int s) {
+    if (nt == 32) __syncwarp();
+    if (leader && at_row.ok && i + S < q.count) issue(t + S * q.step, s);
+  };
   for (int i = 0; i < q.count; ++i, t += q.step) {
     float r = 1.0f;
     if (HASY && p.gate_tok) r = p.gate_tok[t];
@@ -129,7 +148,8 @@ __global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
         Pair a = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) a = fma2(y[k], y[k], a);
-        r *= rsqrtf(fmaf(row_sum<THREADS>(sums, sum2(a)), p.inv_d, p.eps));
+        r *= rsqrtf(fmaf(row_sum(sums, sum2(a)), p.inv_d, p.eps));
+        refill(i, t, s);
       }
       const Pair rr = pair(r, r);
 #pragma unroll
@@ -148,7 +168,7 @@ __global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
       Pair a = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) a = fma2(x[k], x[k], a);
-      const float r1 = rsqrtf(fmaf(row_sum<THREADS>(sums, sum2(a)), p.inv_d, p.eps));
+      const float r1 = rsqrtf(fmaf(row_sum(sums, sum2(a)), p.inv_d, p.eps));
       const Pair rr = pair(r1, r1);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = mul2(mul2(x[k], rr), wpre[k]);
@@ -157,32 +177,27 @@ __global__ void __launch_bounds__(THREADS, kSmThreads / THREADS)
         put<W>(static_cast<T*>(p.u) + e + v * nt * W, (v * nt + q.lane_t) * W < q.cols,
                x + v * W / 2);
     }
-    // every thread of the team has read the row: the sums' barriers came after
     if (!POST && !PRE) team_sync(q.team, nt);
-    if (nt == 32) __syncwarp();
-    if (leader && at_row.ok && i + S < q.count) issue(t + S * q.step, s);
+    if (!POST) refill(i, t, s);
     at_row.next();
   }
   if (leader) at_row.drain();
   if (p.C > 1) cluster_barrier();  // no CTA leaves while another may write to it
 }
 
-// Stages of the ring: as many as leave room for an SM's threads, 2 to 4.
-template <typename T, int THREADS, bool HASY, bool POST, bool FULL, bool PRE>
-int run_threads(const NormFwd& p0, cudaStream_t st) {
-  static std::atomic<bool> configured[kMaxDevices];
-  constexpr int row = kCols * (int)sizeof(T) * (1 + HASY + FULL);
-  constexpr int fit = kNormSmem / (row * kSmThreads), S = fit > 4 ? 4 : fit;
+template <typename T, bool HASY, bool POST, bool FULL, bool PRE>
+int run_fwd(const NormFwd& p0, cudaStream_t st) {
+  static NormSetup setup;
+  constexpr int stage = kCols * (int)sizeof(T) * (1 + HASY + FULL);
+  static_assert(kFwdStages * stage * kNormThreads * kFwdCtas <= kNormSmem, "two CTAs per SM");
   NormFwd p = p0;
-  const NormPlan q = norm_plan(p.T, p.d, S * row, THREADS);
+  NormPlan q = norm_plan(p.T, p.d, kFwdStages * stage, kFwdCtas);
+  const auto kernel = block_norm_fwd<T, HASY, POST, FULL, PRE>;
+  const int rc = prepare_norm(kernel, setup, q);
+  if (rc != MOE_OK) return rc;
   p.C = q.C;
   p.nt = q.nt;
-  return launch_norm(block_norm_fwd<T, THREADS, S, HASY, POST, FULL, PRE>, configured, p, q, st);
-}
-template <typename T, bool HASY, bool POST, bool FULL, bool PRE>
-int run_fwd(const NormFwd& p, cudaStream_t st) {
-  return norm_wide(p.T, p.d, 4096) ? run_threads<T, kWideThreads, HASY, POST, FULL, PRE>(p, st)
-                             : run_threads<T, kNormThreads, HASY, POST, FULL, PRE>(p, st);
+  return launch_norm(kernel, p, q, st);
 }
 
 template <typename T>

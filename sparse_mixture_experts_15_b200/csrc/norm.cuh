@@ -1,6 +1,6 @@
 // Pieces of the block-norm kernels (norm.cu, norm_bwd.cu).
 //
-// A team of nt threads (a multiple of 32, at most 512) takes a row, 16 columns a
+// A team of nt threads (a multiple of 32, at most 256) takes a row, 16 columns a
 // thread, so that the fixed work of a row (its sums' shuffles, the barriers, the
 // addresses) is spread over many columns; teams walk the rows with a stride.
 // One thread of a team starts bulk copies of the next rows into a ring in
@@ -8,10 +8,9 @@
 // instructions of the other threads.  (Copies by every thread, cp.async, reached
 // the same bandwidth alone, but not next to the row's arithmetic: 136 us against
 // 106 for the gradients of 8192 x 4096 bf16 with fp32 stream gradients.)
-// Arithmetic is on pairs (one instruction for two fp32 operations).  Two CTAs
-// of 256 threads share an SM for rows of up to 4096 columns; wider rows take
-// CTAs of 512 (norm_wide), and where that isn't enough a cluster of two, whose
-// sums go through distributed shared memory.
+// Arithmetic is on pairs (one instruction for two fp32 operations).  Rows
+// above 4096 columns go to a cluster of two or four CTAs that exchange their sums
+// through distributed shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -20,9 +19,8 @@
 
 namespace moe {
 
-constexpr int kNormThreads = 256, kWideThreads = 512;
-constexpr int kSmThreads = 512;        // of an SM: what 128 registers a thread leave room for
-constexpr int kNormMaxD = 16384;       // a cluster of 2 CTAs of 512 threads x 16 columns
+constexpr int kNormThreads = 256;
+constexpr int kNormMaxD = 16384;       // a cluster of 4 CTAs of 256 threads x 16 columns
 constexpr int kNormSmem = 200 * 1024;  // dynamic shared memory of an SM that the CTAs take, at most
 
 namespace {
@@ -152,7 +150,7 @@ __device__ __forceinline__ void gains(const Place& q, int nt, const float* a, co
 // that its first thread starts; a stage's barrier completes when they landed.
 // Columns that the row does not have stay the zeros they are set to here.
 constexpr long long kRowWait = 4000000000LL;  // cycles (~2 s)
-constexpr int kMaxTeams = kNormThreads / 32;  // (a wide CTA is one team)
+constexpr int kMaxTeams = kNormThreads / 32;
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -217,7 +215,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // The exchange of a cluster's sums: a CTA's values go to every CTA of the
 // cluster by stores that count on the receiver's barrier, two barriers in turn.
 // (A cluster barrier instead orders the row's stores to global memory first,
-// which takes longer than the sums: 4096 bf16 rows of 16384, both norms, 190 us.)
+// which takes longer than the sums.)
 // A barrier's next use can't begin early: a CTA sends use k + 2 after it has all
 // of use k + 1, and this CTA's part of that is sent after all its threads are
 // past use k.  A wait that runs out records an error, once, and later ones do
@@ -272,32 +270,22 @@ struct NormPlan {
   size_t smem;
 };
 
-// Rows for CTAs of 512 threads: a sum over a CTA costs less than one over a
-// cluster, and 8192 columns need none (4096 bf16 rows of 8192, both norms: 57.7
-// us, clusters of two CTAs of 256 89.3; of 16384, clusters of two 190, of four
-// 323).  Up to 4096 columns two CTAs an SM hide one another's barriers (8192 x
-// 4096: 44.9 us, one of 512 48.0), and above 8192 more, smaller CTAs take a few
-// rows faster (one row of 16384: 3.8 and 5.4 us).
-// above: columns from which they are taken (the gradients: 5120, as clusters of two
-// have three CTAs on an SM up to there, 4096 rows 92.1 us and 96.8; of 6144 117.6
-// and 106.7).
-inline bool norm_wide(int T, int d, int above) {
-  return d > above && (d <= 16 * kWideThreads || T > sm_count() / 2);
-}
-
-// bytes: of the ring per thread.  threads: of a CTA, at most.  Few rows are
-// spread over the SMs before a CTA gets a second team.
-inline NormPlan norm_plan(int T, int d, int bytes, int threads) {
+// bytes: of the ring per thread.  ctas: CTAs of 256 threads per SM.  Few rows
+// are spread over the SMs before a CTA gets a second team.
+inline NormPlan norm_plan(int T, int d, int bytes, int ctas) {
   NormPlan q;
   const int sms = sm_count(), chunks = d / 8;
-  q.C = chunks <= 2 * threads ? 1 : chunks <= 4 * threads ? 2 : 4;
+  // (three CTAs, where they fill an SM's threads better, are slower: 4096 bf16 rows
+  // of 6144, both norms, 56.0 us, two 48.5; of 12288 95.0 where four take 113.6,
+  // but the gradients 257 and 186)
+  q.C = chunks <= 2 * kNormThreads ? 1 : chunks <= 4 * kNormThreads ? 2 : 4;
   q.nt = ((chunks + 2 * q.C - 1) / (2 * q.C) + 31) / 32 * 32;
-  int teams = threads / q.nt;
+  int teams = kNormThreads / q.nt;
   const int spread = (T + sms - 1) / sms;
   if (teams > spread) teams = spread;
   q.block = teams * q.nt;
   q.smem = (size_t)bytes * q.block;
-  int per_sm = kSmThreads / q.block;
+  int per_sm = kNormThreads * ctas / q.block;
   const int fit = (int)(kNormSmem / q.smem);
   if (per_sm > fit) per_sm = fit;
   const int64_t want = (int64_t)((T + teams - 1) / teams) * q.C;
@@ -306,35 +294,77 @@ inline NormPlan norm_plan(int T, int d, int bytes, int threads) {
   return q;
 }
 
-// Launches a block-norm kernel, with its shared-memory attribute set once per
-// device and instantiation.
-template <typename P>
-int launch_norm(void (*kernel)(P), std::atomic<bool>* configured, const P& p, const NormPlan& q,
-                cudaStream_t st) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || !device_slot(dev)) return MOE_ERR_CUDA;
-  if (needs_setup(configured, dev)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem) !=
-        cudaSuccess)
-      return MOE_ERR_CUDA;
-    cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                         (int)cudaSharedmemCarveoutMaxShared);
-    mark_setup(configured, dev);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)q.grid);
-  cfg.blockDim = dim3((unsigned)q.block);
-  cfg.dynamicSmemBytes = q.smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
+// What an instantiation keeps per device: whether its attributes are set, and the
+// last plan's clusters that can run at once (block << 40 | C << 32 | clusters).
+struct NormSetup {
+  std::atomic<bool> configured[kMaxDevices];
+  std::atomic<uint64_t> resident[kMaxDevices];
+};
+
+inline void norm_config(const NormPlan& q, cudaStream_t st, cudaLaunchConfig_t* cfg,
+                        cudaLaunchAttribute* attr) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3((unsigned)q.grid);
+  cfg->blockDim = dim3((unsigned)q.block);
+  cfg->dynamicSmemBytes = q.smem;
+  cfg->stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = q.C;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = q.C > 1 ? 2 : 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = q.C > 1 ? 2 : 1;
+}
+
+// Sets a kernel's attributes, once, and takes from the plan's grid the clusters
+// that would not run at once with the others: a cluster's CTAs share a GPC, whose
+// SMs they may not divide evenly, and the rows are dealt out beforehand, so a
+// cluster left over would take as long again as all the others.  (4096 bf16 rows
+// of 16384, both norms: 118 us, the whole grid 207, and 323 with cluster barriers
+// for the sums.  CTAs of 512 threads, whose rows of 8192 need no cluster, took
+// 56.8 us for those, two of 256 57.4, and the gradients 123 and 107.)
+template <typename P>
+int prepare_norm(void (*kernel)(P), NormSetup& set, NormPlan& q) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !device_slot(dev)) return MOE_ERR_CUDA;
+  if (needs_setup(set.configured, dev)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                         (int)cudaSharedmemCarveoutMaxShared);
+    mark_setup(set.configured, dev);
+  }
+  if (q.C == 1) return MOE_OK;
+  const uint64_t key = ((uint64_t)q.block << 8 | (uint64_t)q.C) << 32;
+  uint64_t known = set.resident[dev].load(std::memory_order_relaxed);
+  if ((known & ~0xFFFFFFFFull) != key) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    norm_config(q, nullptr, &cfg, attr);
+    cfg.gridDim = dim3((unsigned)(16 * sm_count() / q.C * q.C));
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    known = key | (uint64_t)n;
+    set.resident[dev].store(known, std::memory_order_relaxed);
+  }
+  const int64_t most = (int64_t)(known & 0xFFFFFFFFull) * q.C;
+  if (q.grid > most) q.grid = (int)most;
+  return MOE_OK;
+}
+
+template <typename P>
+int launch_norm(void (*kernel)(P), const P& p, const NormPlan& q, cudaStream_t st) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  norm_config(q, st, &cfg, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) pdl_launch_error() = e;
   return launch_status();
