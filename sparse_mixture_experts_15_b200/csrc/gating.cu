@@ -173,10 +173,10 @@ struct SelectParams {
 // of it.  Where more than 32 qualify (ties, k near 32), the k are taken one
 // after another instead.
 //
-// Bound by the issue of its arithmetic: of some 1050 instructions a token (256
+// Bound by the issue of its arithmetic: of some 990 instructions a token (256
 // experts, 8 groups, top-8) the scores in double are a quarter.  Selecting on
 // fp32 scores, with exact ones where two lie within their error, was no faster
-// (12.9 us for 8192 tokens, 11.4 here): the checks cost what the doubles do.
+// (12.9 us for 8192 tokens, 10.6 here): the checks cost what the doubles do.
 template <int PER>
 __global__ void __launch_bounds__(32 * kSelWarps, PER >= 24 ? 7 : 1)
     route_select(const __grid_constant__ SelectParams p) {
