@@ -254,6 +254,20 @@ def test_wide_rows(T, d):
         check_backward(t, DT[grad], T)
 
 
+@pytest.mark.parametrize("T,d", [(200, 8192), (3, 16384)])
+def test_wide_rows_captured(T, d):
+    """Clusters in a graph, as a call outside it does."""
+    t = inputs(T, d, torch.float16, "token", True, True, 3)
+    want = forward(t)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = forward(t)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_backward_without_stream_gradient_or_branch():
     t = inputs(33, 1000, torch.bfloat16, "channel", True, True, 1)
     check_backward(t, torch.float32, 2, dxo_none=True)

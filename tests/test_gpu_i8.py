@@ -129,6 +129,15 @@ def test_grouped_product(counts, dtype):
         check(counts, K, n, dtype, seed=i, extra=i % 2 * 9)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("counts,K,n", [([1000, 700, 0, 901], 640, 2570), ([150, 161, 33, 200], 656, 5003),
+                                        ([900, 301], 512, 2001), ([2500], 2064, 1000)])
+def test_many_tiles(counts, K, n, dtype):
+    """Several rounds of tiles over the SMs: on pairs of CTAs, of either width, and
+    on single ones."""
+    check(counts, K, n, dtype, seed=K)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 8, 17, 32, 60])
 @pytest.mark.parametrize("K,n", [(4096, 4096), (4112, 1000), (14336, 264), (256, 14336), (64, 3)])
 def test_few_rows(rows, K, n):
