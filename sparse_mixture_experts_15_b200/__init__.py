@@ -623,20 +623,29 @@ def _run(fn, dev, stream, *args):
         raise MoeError(rc, fn.__name__)
 
 
+def _on_stream(cuda, stream, dev):
+    """The context in which the allocator's memory is that of a stream given by
+    its handle (0 and 1: the default stream, which is no external one)."""
+    return cuda.stream(cuda.default_stream(dev) if stream in (0, 1)
+                       else cuda.ExternalStream(stream, device=dev))
+
+
 def _workspace(ws, dev, stream, query, *args):
     """(address, bytes, tensor) of a workspace: the caller's, whose size the
-    library checks, or one of the queried size, which a given stream then holds
-    until its work so far is done; keep the tensor until the call is made."""
+    library checks, or one of the queried size from the memory of the stream that
+    the call runs on.  (A block of another stream's memory may still be in use
+    there, by a call before this one.)  Keep the tensor until the call is made."""
     if ws is None:
-        cuda = _t.torch.cuda
-        with cuda.device(dev):
+        torch = _t.torch
+        with torch.cuda.device(dev):
             n = int(query(*args))
-        if n == 0:
-            return None, 0, None
-        ws = _t.torch.empty(max(n, 256), dtype=_t.torch.uint8, device=f"cuda:{dev}")
-        if stream is not None and int(stream) != _t.raw_stream(dev):
-            # it is from the current stream's memory, and used on another
-            ws.record_stream(cuda.ExternalStream(int(stream), device=dev))
+            if n == 0:
+                return None, 0, None
+            if stream is None or int(stream) == _t.raw_stream(dev):
+                ws = torch.empty(max(n, 256), dtype=torch.uint8, device=f"cuda:{dev}")
+            else:
+                with _on_stream(torch.cuda, int(stream), dev):
+                    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=f"cuda:{dev}")
     elif ws.get_device() != dev:
         raise ValueError(f"ws: on {ws.device}, the call's tensors on cuda:{dev}")
     return _ptr(ws), ws.numel() * ws.element_size(), ws

@@ -1,0 +1,103 @@
+"""Which stream the workspace of a call belongs to: memory that a call allocates
+for itself must be the allocator's for the stream that the call runs on.  From
+another stream's memory it may be a block whose last user, still queued there,
+writes while the call reads.  On the host, with the allocator's calls recorded."""
+import contextlib
+import ctypes
+import types
+
+import pytest
+import torch
+
+import sparse_mixture_experts_15_b200 as moe
+
+CURRENT, SIDE, DEFAULT = 0x7100, 0x7200, 0
+
+
+class Recorder:
+    """torch as the binding uses it for a workspace; `used` is the streams that
+    were current when memory was taken."""
+
+    uint8 = torch.uint8
+
+    def __init__(self):
+        self.now, self.used = [CURRENT], []
+        self.cuda = types.SimpleNamespace(
+            device=lambda dev: contextlib.nullcontext(), stream=self._stream,
+            ExternalStream=lambda handle, device=None: self._known(handle),
+            default_stream=lambda device=None: DEFAULT,
+            current_stream=lambda device=None: types.SimpleNamespace(cuda_stream=self.now[-1]))
+
+    @staticmethod
+    def _known(handle):
+        assert handle != 0  # an ExternalStream of no handle is a stream of its own
+        return handle
+
+    @contextlib.contextmanager
+    def _stream(self, s):
+        self.now.append(s)
+        yield
+        self.now.pop()
+
+    def empty(self, n, dtype=None, device=None):
+        self.used.append(self.now[-1])
+        t = types.SimpleNamespace(is_cuda=True, is_contiguous=lambda: True, data_ptr=lambda: 4096,
+                                  numel=lambda: n, element_size=lambda: 1)
+        return t
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    r = Recorder()
+    moe._t.act  # looks torch up, so that nothing is set again below
+    monkeypatch.setattr(moe._t, "torch", r)
+    monkeypatch.setattr(moe._t, "raw_stream", lambda dev: r.now[-1])
+    return r
+
+
+@pytest.mark.parametrize("stream,owner", [(None, CURRENT), (CURRENT, CURRENT), (SIDE, SIDE),
+                                          (0, DEFAULT)])
+def test_a_workspace_is_of_the_calls_stream(fake, stream, owner):
+    b = moe.block_norm(64, 256)
+    p, n, ws = moe._workspace(None, 0, stream, moe._lib.moe_block_norm_bwd_workspace_bytes,
+                              ctypes.byref(b))
+    assert p == 4096 and n >= 2 * 256 * 4 and ws is not None
+    assert fake.used == [owner]
+    assert fake.now == [CURRENT]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("side", ["own", "default"])
+def test_calls_on_two_streams_do_not_share_a_workspace(side):
+    """A call on the current stream, its kernels still queued, then one on another
+    stream: each takes its workspace itself, and nothing orders the two streams."""
+    T, d = 3000, 1024
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, y, dxo, du = (torch.randn(T, d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    w = 1 + torch.randn(d, generator=g, device="cuda") * 0.1
+    x2, du2 = (3 * torch.randn(T, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    b = moe.block_norm(T, d)
+
+    def outputs():
+        return dict(dx=torch.empty_like(x), dy=torch.empty_like(x),
+                    dw_post=torch.empty(d, device="cuda"), dw_pre=torch.empty(d, device="cuda"))
+
+    def call(out, x_out, grad, stream=None):
+        moe.moe_block_norm_bwd(b, dxo, out, x_out=x_out, y=y, w_post=w, w_pre=w, du=grad,
+                               stream=stream)
+
+    ref, ref2 = outputs(), outputs()
+    call(ref, x, du)
+    call(ref2, x2, du2)
+    a, c = outputs(), outputs()
+    torch.cuda.synchronize()
+    here = torch.cuda.Stream()
+    there = torch.cuda.Stream().cuda_stream if side == "own" else 0
+    with torch.cuda.stream(here):
+        for _ in range(20):
+            call(a, x, du)
+            call(c, x2, du2, there)
+    torch.cuda.synchronize()
+    for k in ref:
+        assert torch.equal(a[k], ref[k]) and torch.equal(c[k], ref2[k])
+    assert moe.moe_device_status() == 0
