@@ -258,14 +258,27 @@ def _dtype_code(t):
     return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[t.dtype]
 
 
-def _ws(nbytes, device, ws=None):
+def _on_stream(cuda, stream, dev):
+    """The context in which the allocator's memory is that of a stream given by
+    its handle (0 and 1: the default stream, which is no external one)."""
+    return cuda.stream(cuda.default_stream(dev) if stream in (0, 1)
+                       else cuda.ExternalStream(stream, device=dev))
+
+
+def _ws(nbytes, device, ws=None, stream=None):
+    """(tensor, bytes) of a workspace: the caller's, or one from the memory of the
+    stream that the call runs on (a block of another stream's memory may still be
+    in use there)."""
     import torch
     if ws is not None:
         if ws.numel() * ws.element_size() < nbytes:
             raise MoeError(-6, "workspace")
         return ws, ws.numel() * ws.element_size()
     n = max(int(nbytes), 256)
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+    if stream is None or int(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(n, dtype=torch.uint8, device=device), n
+    with _on_stream(torch.cuda, int(stream), device):
+        return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
 def shape(T, d, N, k, h=0, renorm=1, capacity=0) -> MoeShape:
@@ -299,7 +312,7 @@ def moe_route(s: MoeShape, u, w_route, top_idx, top_w, bias=None, probs=None, lo
                  ("logits", logits, s.T * s.N, _F32)):
         _need(*args)
     nb = _lib.moe_route_workspace_bytes(ctypes.byref(s))
-    wbuf, wlen = (None, 0) if logits is not None else _ws(nb, u.device, ws)
+    wbuf, wlen = (None, 0) if logits is not None else _ws(nb, u.device, ws, stream)
     _check(_lib.moe_route(ctypes.byref(s), _ptr(u), _dtype_code(u), _ptr(w_route), _ptr(bias),
                           _ptr(top_idx), _ptr(top_w), _ptr(probs), _ptr(logits), _ptr(wbuf), wlen,
                           _stream(stream)), "moe_route")
@@ -313,7 +326,7 @@ def moe_aux_stats(probs, top_idx, f=None, P=None, n_sum_fP=None, loads=None, ws=
                  ("f", f, N, _F32), ("P", P, N, _F32), ("n_sum_fP", n_sum_fP, 1, _F32),
                  ("loads", loads, N, _I32)):
         _need(*args)
-    wbuf, wlen = _ws(_lib.moe_aux_stats_workspace_bytes(N), top_idx.device, ws)
+    wbuf, wlen = _ws(_lib.moe_aux_stats_workspace_bytes(N), top_idx.device, ws, stream)
     _check(_lib.moe_aux_stats(T, N, k, _ptr(probs), _ptr(top_idx), _ptr(f), _ptr(P),
                               _ptr(n_sum_fP), _ptr(loads), _ptr(wbuf), wlen, _stream(stream)),
            "moe_aux_stats")
@@ -330,7 +343,7 @@ def _permute_sizes(s, top_idx, counts, offsets, perm_tok, row_of, overflow, tota
 def moe_permute(s: MoeShape, top_idx, counts, offsets, perm_tok, row_of, overflow, totals,
                 ws=None, stream=None):
     _permute_sizes(s, top_idx, counts, offsets, perm_tok, row_of, overflow, totals)
-    wbuf, wlen = _ws(_lib.moe_permute_workspace_bytes(ctypes.byref(s)), top_idx.device, ws)
+    wbuf, wlen = _ws(_lib.moe_permute_workspace_bytes(ctypes.byref(s)), top_idx.device, ws, stream)
     _check(_lib.moe_permute(ctypes.byref(s), _ptr(top_idx), _ptr(counts), _ptr(offsets),
                             _ptr(perm_tok), _ptr(row_of), _ptr(overflow), _ptr(totals), _ptr(wbuf),
                             wlen, _stream(stream)), "moe_permute")
@@ -369,7 +382,7 @@ def moe_expert_ffn(s: MoeShape, width: int, x_rows, offsets, w_gate, w_up, w_dow
         _need(*args)
     dt = _dtype_code(x_rows)
     nb = _lib.moe_expert_ffn_workspace_bytes(ctypes.byref(s), width, dt)
-    wbuf, wlen = _ws(nb, x_rows.device, ws)
+    wbuf, wlen = _ws(nb, x_rows.device, ws, stream)
     _check(_lib.moe_expert_ffn(ctypes.byref(s), width, _ptr(x_rows), dt, _ptr(offsets),
                                _ptr(w_gate), _ptr(w_up), _ptr(w_down), _dtype_code(w_gate),
                                ctypes.byref(a), _ptr(y_rows), _ptr(wbuf), wlen, _stream(stream)),
@@ -403,7 +416,7 @@ def moe_layer_fwd(s: MoeShape, w_route, w_gate, w_up, w_down, u, y, bias=None, a
     O = _outputs(s, outputs)
     W = MoeLayerWeights(_ptr(w_route), _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                         _dtype_code(w_gate), a)
-    wbuf, wlen = _ws(moe_layer_workspace_bytes(s, dt), u.device, ws)
+    wbuf, wlen = _ws(moe_layer_workspace_bytes(s, dt), u.device, ws, stream)
     _check(_lib.moe_layer_fwd(ctypes.byref(s), ctypes.byref(W), _ptr(u), dt, _ptr(y),
                               ctypes.byref(O), _ptr(wbuf), wlen, _stream(stream)), "moe_layer_fwd")
 
@@ -438,7 +451,7 @@ def moe_layer_bwd(s: MoeShape, w_route, w_gate, w_up, w_down, u, dy, fwd: dict, 
     O = _outputs(s, fwd)
     G = MoeLayerGrads(*(_ptr(grads.get(n)) for n in ("du", "dz", "dw_route", "dw_gate", "dw_up",
                                                      "dw_down")))
-    wbuf, wlen = _ws(moe_layer_bwd_workspace_bytes(s), u.device, ws)
+    wbuf, wlen = _ws(moe_layer_bwd_workspace_bytes(s), u.device, ws, stream)
     _check(_lib.moe_layer_bwd(ctypes.byref(s), ctypes.byref(W), _ptr(u), _ptr(dy),
                               ctypes.byref(O), alpha, _ptr(f), ctypes.byref(G), _ptr(wbuf), wlen,
                               _stream(stream)), "moe_layer_bwd")
@@ -467,7 +480,7 @@ def moe_latent_fwd(s: MoeShape, w_route, w_gate, w_up, w_down, lw: MoeLatentWeig
     O = _outputs(s, outputs)
     W = MoeLayerWeights(_ptr(w_route), _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down), BF16,
                         a)
-    wbuf, wlen = _ws(moe_latent_workspace_bytes(s, lw), x.device, ws)
+    wbuf, wlen = _ws(moe_latent_workspace_bytes(s, lw), x.device, ws, stream)
     _check(_lib.moe_latent_fwd(ctypes.byref(s), ctypes.byref(W), ctypes.byref(lw), _ptr(x),
                                _ptr(y), ctypes.byref(O), _ptr(wbuf), wlen, _stream(stream)),
            "moe_latent_fwd")
@@ -493,7 +506,7 @@ def moe_latent_bwd(s: MoeShape, w_route, w_gate, w_up, w_down, lw: MoeLatentWeig
     O = _outputs(s, fwd)
     G = MoeLatentGrads(*(_ptr(grads.get(k)) for k in sizes))
     wbuf, wlen = _ws(int(_lib.moe_latent_bwd_workspace_bytes(ctypes.byref(s), ctypes.byref(lw))),
-                     x.device, ws)
+                     x.device, ws, stream)
     _check(_lib.moe_latent_bwd(ctypes.byref(s), ctypes.byref(W), ctypes.byref(lw), _ptr(x),
                                _ptr(dy), ctypes.byref(O), ctypes.byref(G), _ptr(wbuf), wlen,
                                _stream(stream)), "moe_latent_bwd")
@@ -533,7 +546,7 @@ def moe_expert_ffn_e4m3(s: MoeShape, width: int, x_rows, x_scale, offsets, w_gat
         _need(*args)
     sc = MoeE4M3Scales(_ptr(gate_scale), _ptr(up_scale), _ptr(down_scale))
     wbuf, wlen = _ws(int(_lib.moe_expert_ffn_e4m3_workspace_bytes(ctypes.byref(s))),
-                     x_rows.device, ws)
+                     x_rows.device, ws, stream)
     _check(_lib.moe_expert_ffn_e4m3(ctypes.byref(s), width, _ptr(x_rows), _ptr(x_scale),
                                     _ptr(offsets), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                     ctypes.byref(sc), ctypes.byref(a), _ptr(y_rows), _ptr(wbuf),
@@ -558,7 +571,7 @@ def moe_latent_fwd_e4m3(s: MoeShape, w_route, w_gate, w_up, w_down, gate_scale, 
     W = MoeLayerWeights(_ptr(w_route), _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down), E4M3,
                         a)
     sc = MoeE4M3Scales(_ptr(gate_scale), _ptr(up_scale), _ptr(down_scale))
-    wbuf, wlen = _ws(moe_latent_workspace_bytes(s, lw), x.device, ws)
+    wbuf, wlen = _ws(moe_latent_workspace_bytes(s, lw), x.device, ws, stream)
     _check(_lib.moe_latent_fwd_e4m3(ctypes.byref(s), ctypes.byref(W), ctypes.byref(sc),
                                     ctypes.byref(lw), _ptr(x), _ptr(y), ctypes.byref(O),
                                     _ptr(wbuf), wlen, _stream(stream)), "moe_latent_fwd_e4m3")
@@ -621,13 +634,6 @@ def _run(fn, dev, stream, *args):
             rc = fn(*args, stream)
     if rc != 0:
         raise MoeError(rc, fn.__name__)
-
-
-def _on_stream(cuda, stream, dev):
-    """The context in which the allocator's memory is that of a stream given by
-    its handle (0 and 1: the default stream, which is no external one)."""
-    return cuda.stream(cuda.default_stream(dev) if stream in (0, 1)
-                       else cuda.ExternalStream(stream, device=dev))
 
 
 def _workspace(ws, dev, stream, query, *args):
@@ -820,7 +826,7 @@ def moe_decode_layer(s: MoeShape, layer: MoeQ4Layer, u, y, u_next=None, top_idx=
                  ("u_next", u_next, s.T * s.d, _F16), ("top_idx", top_idx, s.T * s.k, _I32),
                  ("top_w", top_w, s.T * s.k, _F32)):
         _need(*args)
-    wbuf, wlen = _ws(moe_decode_workspace_bytes(s), u.device, ws)
+    wbuf, wlen = _ws(moe_decode_workspace_bytes(s), u.device, ws, stream)
     _check(_lib.moe_decode_layer(ctypes.byref(s), ctypes.byref(layer), _ptr(u), _ptr(y),
                                  _ptr(u_next), _ptr(top_idx), _ptr(top_w), _ptr(wbuf), wlen,
                                  _stream(stream)), "moe_decode_layer")
@@ -832,7 +838,7 @@ def moe_decode_step(s: MoeShape, layers, u0, u_out, top_idx_all=None, ws=None, s
                  ("top_idx_all", top_idx_all, len(layers) * s.T * s.k, _I32)):
         _need(*args)
     arr = (MoeQ4Layer * len(layers))(*layers)
-    wbuf, wlen = _ws(moe_decode_workspace_bytes(s), u0.device, ws)
+    wbuf, wlen = _ws(moe_decode_workspace_bytes(s), u0.device, ws, stream)
     _check(_lib.moe_decode_step(ctypes.byref(s), len(layers), arr, _ptr(u0), _ptr(u_out),
                                 _ptr(top_idx_all), _ptr(wbuf), wlen, _stream(stream)),
            "moe_decode_step")
@@ -851,7 +857,7 @@ def moe_decode_step_trace(s: MoeShape, layers, u0, u_out, stamps, top_idx_all=No
                  ("stamps", stamps, DECODE_STAMPS * len(layers), "int64")):
         _need(*args)
     arr = (MoeQ4Layer * len(layers))(*layers)
-    wbuf, wlen = _ws(moe_decode_workspace_bytes(s), u0.device, ws)
+    wbuf, wlen = _ws(moe_decode_workspace_bytes(s), u0.device, ws, stream)
     _check(_lib.moe_decode_step_trace(ctypes.byref(s), len(layers), arr, _ptr(u0), _ptr(u_out),
                                       _ptr(top_idx_all), _ptr(wbuf), wlen, _ptr(stamps),
                                       _stream(stream)), "moe_decode_step_trace")
@@ -879,7 +885,7 @@ def moe_quantile_balance(scores, k: int, q: int, bias_exact, bias=None, bins: in
                  ("bias", bias, N, _F32), ("cutoff", cutoff, T, _F32),
                  ("bias_hist", bias_hist, N, _F32), ("loads", loads, N, _I32)):
         _need(*args)
-    wbuf, wlen = _ws(moe_quantile_balance_workspace_bytes(T, N), scores.device, ws)
+    wbuf, wlen = _ws(moe_quantile_balance_workspace_bytes(T, N), scores.device, ws, stream)
     _check(_lib.moe_quantile_balance(T, N, k, _ptr(scores), _ptr(bias), q, bins, _ptr(cutoff),
                                      _ptr(bias_exact), _ptr(bias_hist), _ptr(loads), _ptr(wbuf),
                                      wlen, _stream(stream)), "moe_quantile_balance")

@@ -101,3 +101,43 @@ def test_calls_on_two_streams_do_not_share_a_workspace(side):
     for k in ref:
         assert torch.equal(a[k], ref[k]) and torch.equal(c[k], ref2[k])
     assert moe.moe_device_status() == 0
+
+
+class Tensor:
+    """A CUDA tensor as the binding sees it."""
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape, self.device, self.is_cuda = dtype, shape, "cuda:0", True
+
+    def numel(self):
+        return int(torch.Size(self.shape).numel())
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.mark.parametrize("name,args", [
+    ("moe_route", lambda s, f, i, h: (s, f(16, 64), f(8, 64), i(16, 2), f(16, 2))),
+    ("moe_aux_stats", lambda s, f, i, h: (f(16, 8), i(16, 2), f(8))),
+    ("moe_permute", lambda s, f, i, h: (s, i(16, 2), i(8), i(9), i(32), i(32), i(8), i(3))),
+    ("moe_expert_ffn", lambda s, f, i, h: (s, 128, h(32, 128), i(9), *(h(8, 128, 128),) * 3,
+                                           f(32, 128))),
+    ("moe_layer_fwd", lambda s, f, i, h: (s, f(8, 64), *(h(8, 128, 64),) * 3, h(16, 64),
+                                          h(16, 64))),
+    ("moe_quantile_balance", lambda s, f, i, h: (f(16, 8), 2, 4, f(8))),
+])
+@pytest.mark.parametrize("stream,owner", [(None, CURRENT), (CURRENT, CURRENT), (SIDE, SIDE),
+                                          (0, DEFAULT)])
+def test_every_calls_workspace_is_of_its_stream(fake, monkeypatch, name, args, stream, owner):
+    """The layer's own calls, with the library's launch left out."""
+    make = [lambda *n, dt=dt: Tensor(dt, *n) for dt in (torch.float32, torch.int32, torch.bfloat16)]
+    launched = []
+    monkeypatch.setattr(moe._lib, name, lambda *a: launched.append(a[-1]) or 0)
+    for attr in ("cuda", "empty"):
+        monkeypatch.setattr(torch, attr, getattr(fake, attr))
+    getattr(moe, name)(*args(moe.shape(16, 64, 8, 2, 128), *make), stream=stream)
+    assert fake.used == [owner]
+    assert launched == [CURRENT if stream is None else stream]
