@@ -374,6 +374,57 @@ struct SelectBwdParams {
   int* status;
 };
 
+// Adds what renormalised weights give to dz of a row whose selected scores sum to
+// little: with w_i = s_i / S
+//   w_i (da_i - sum da w) (1 - s_i)       softmax: without 1 - s_i, since the slots'
+//                                         part of sum g s is 0
+// A bias or the groups can select scores near fp32's smallest, where s / S keeps
+// few bits and 1 / S overflows; so w comes from the logits z relative to the
+// largest selected one.  Where every selected score rounds to 0 in fp32 (150 ln 2
+// below 1), the weights are 0.
+__device__ __forceinline__ void add_tiny_part(const SelectBwdParams& p, int64_t t, int lane) {
+  constexpr float kNoScore = -103.972084f;  // the value below -150 ln 2
+  const float* row = p.logits + t * p.N;
+  int idx = lane < p.k ? p.top_idx[t * p.k + lane] : -1;
+  if (idx >= p.N) idx = -1;
+  const float z = idx >= 0 ? row[idx] : -INFINITY;
+  const float da = idx >= 0 ? p.d_top_w[t * p.k + lane] * p.scale : 0.0f;
+  float top = z;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float log_top = top;  // of the largest selected score
+  if (!p.sigmoid) {
+    float m = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int j = lane; j < p.N; j += 32) m = fmaxf(m, row[j]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 1
+    for (int j = lane; j < p.N; j += 32) sum += expf(row[j] - m);
+    log_top = top - m - logf(warp_sum(sum));
+  }
+  if (top == -INFINITY || log_top <= kNoScore) return;
+  const float x = p.sigmoid ? expf(-fabsf(z)) : 0.0f, q = 1.0f / (1.0f + x);
+  if (p.sigmoid) top = fminf(top, 0.0f);
+  // s_i over e^top (sigmoid) or over the largest selected score
+  float w = p.sigmoid && z >= 0.0f ? q : expf(z - top) * q;
+  w /= warp_sum(w);
+  const float mean = warp_sum(w * da);
+  const float part = w * (da - mean) * (p.sigmoid && z >= 0.0f ? x * q : q);
+  float sum = 0.0f;
+  int first = 32;
+#pragma unroll 1
+  for (int r = 0; r < p.k; ++r) {
+    const int ir = __shfl_sync(0xffffffffu, idx, r);
+    const float pr = __shfl_sync(0xffffffffu, part, r);
+    if (ir == idx) {
+      sum += pr;
+      first = min(first, r);
+    }
+  }
+  if (idx >= 0 && first == lane) p.dz[t * p.N + idx] += sum;
+}
+
 // One warp per token.  With g_j = dL/ds_j (d_scores plus what the weights of
 // the selected experts give):
 //   renorm: dL/ds_i = scale (da_i - sum_l da_l s_l / S) / S;  else scale da_i
@@ -457,9 +508,13 @@ __global__ void __launch_bounds__(32 * kSelWarps, PER <= 28 ? 7 : 6)
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   // the selected experts' part; an index that is there twice counts twice
+  bool tiny = false;  // of the whole row
   if (p.renorm) {
     const float s = idx >= 0 ? ss[idx] : 0.0f, S = warp_sum(s), ds = warp_sum(da * s);
-    da = S == 0.0f || idx < 0 ? 0.0f : (da - ds / S) / S;
+    // above the bound a subnormal score is 2^-62 of the sum at most, and nothing
+    // below 2^62 overflows
+    tiny = S < 5.421011e-20f;  // 2^-64
+    da = tiny || idx < 0 ? 0.0f : (da - ds / S) / S;
   }
   float sum = 0.0f;
   int first = 32;
@@ -484,6 +539,9 @@ __global__ void __launch_bounds__(32 * kSelWarps, PER <= 28 ? 7 : 6)
 #pragma unroll
   for (int e = 0; e < PER; ++e) g[e] = z[e] * (g[e] - dot);
   L::store(p.dz + t * N, N, lane, g);
+  if (!tiny) return;
+  __syncwarp();  // the row is stored before the selected experts' part is added
+  add_tiny_part(p, t, lane);
 }
 
 template <template <int> class K, typename P>

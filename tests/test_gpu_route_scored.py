@@ -345,6 +345,98 @@ def test_gradient_of_repeated_and_masked_experts():
         assert np.all(run_bwd(z, idx, da, None, sigmoid, True, 1.0) == 0)
 
 
+def renorm_grad64(z, idx, da, ds, sigmoid, scale):
+    """dz in 64 bits with the weights from logits relative to the largest selected
+    one, so that no score underflows, and the size of the terms it adds."""
+    z = z.astype(np.float64)
+    row, zs = np.arange(len(z))[:, None], np.take_along_axis(z, idx, 1)
+    m = zs.max(1, keepdims=True)
+    top = np.minimum(m, 0) if sigmoid else m
+    with np.errstate(over="ignore"):
+        w = np.exp(zs - top) / (1 + np.exp(zs)) if sigmoid else np.exp(zs - top)
+        w = w / w.sum(1, keepdims=True)
+        s = exact_scores(z, sigmoid)
+        f = 1 / (1 + np.exp(z)) if sigmoid else np.ones_like(z)
+    da = da.astype(np.float64) * scale
+    wda, wma = (w * da).sum(1, keepdims=True), (w * np.abs(da)).sum(1, keepdims=True)
+    fs = np.take_along_axis(f, idx, 1)
+    g = np.zeros_like(z) if ds is None else ds.astype(np.float64)
+    dot, dotm = ((0.0, 0.0) if sigmoid else
+                 ((g * s).sum(1, keepdims=True), (np.abs(g) * s).sum(1, keepdims=True)))
+    # softmax: the terms w_i (da_i - sum da w) of sum g s, at most 2 sum |da| w in
+    # all, add up to 0 but each is rounded, and every dz_j takes s_j of their sum
+    slots = 0.0 if sigmoid else 2 * wma
+    dz, mag = s * f * (g - dot), s * f * (np.abs(g) + dotm + slots)
+    np.add.at(dz, (row, idx), w * fs * (da - wda))
+    np.add.at(mag, (row, idx), w * fs * (np.abs(da) + wma))
+    return dz, mag
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dense", [False, True])
+def test_gradient_of_tiny_selected_scores(sigmoid, dense):
+    """Selected experts whose scores are near fp32's smallest values or between
+    them (a bias or the groups chose them): the renormalised weights stay of
+    order 1, and so does their gradient.  Bounds: the exponential of a rounded
+    difference (|z_i - max| below 20 among the selected: 24 u), 10 roundings of
+    the sums, 10 of the products and the reciprocal, twice; the dense part as
+    elsewhere, with 2^-140 for its subnormal scores."""
+    rng = np.random.default_rng(12)
+    T, N, k = 19, 70, 6
+    base = np.linspace(-103.5, -20.0, T)[:, None]      # the largest of a row's selected
+    z = rng.standard_normal((T, N)).astype(np.float32)
+    z[:, 0] = 2.0
+    idx = np.stack([1 + rng.permutation(N - 1)[:k] for _ in range(T)])
+    drop = rng.uniform(0, 17, (T, k))
+    drop[:, 3] = 0
+    low = (base - drop) + (0 if sigmoid else np.log(np.exp(z.astype(np.float64)).sum(1,
+                                                                               keepdims=True)))
+    np.put_along_axis(z, idx, low.astype(np.float32), 1)
+    da = rng.standard_normal((T, k)).astype(np.float32)
+    ds = rng.standard_normal((T, N)).astype(np.float32) if dense else None
+    ref, mag = renorm_grad64(z, idx, da, ds, sigmoid, 2.5)
+    got = run_bwd(z, idx, da, ds, sigmoid, True, 2.5)
+    assert np.median(np.abs(ref).max(1)) > 0.1
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - ref) <= 128 * U * mag + 2.0 ** -140)
+    if dense:
+        assert np.array_equal(got, run_bwd(z, idx, da, ds, sigmoid, True, 2.5, in_place=True))
+    # the same index twice, and one that is no expert's beside them
+    idx[:, 4] = idx[:, 3]
+    ref, mag = renorm_grad64(z, idx, da, ds, sigmoid, 2.5)
+    got = run_bwd(z, idx, da, ds, sigmoid, True, 2.5)
+    assert np.all(np.abs(got - ref) <= 128 * U * mag + 2.0 ** -140)
+    bad = np.concatenate([idx, np.full((T, 1), N)], 1)
+    got2 = run_bwd(z, bad, np.concatenate([da, np.ones((T, 1), np.float32)], 1), ds, sigmoid, True,
+                   2.5)
+    assert moe.moe_device_status() == -5
+    moe.moe_reset_device_status()
+    assert np.all(np.abs(got2 - ref) <= 128 * U * mag + 2.0 ** -140)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_gradient_ends_where_the_forwards_weights_do(sigmoid):
+    """The weights are 0, and have no gradient, exactly where every selected
+    score rounds to 0 in fp32 (150 ln 2 = 103.97208 below the sigmoid's 0)."""
+    edge = np.float32(-150 * np.log(2.0))
+    steps = np.arange(-4, 5) * np.spacing(np.abs(edge))
+    z = np.full((len(steps), 40), 1.0, np.float32)
+    lift = 0.0 if sigmoid else 1 + np.log(37.0)
+    z[:, 5:8] = (edge + lift + steps.astype(np.float32)[:, None]).astype(np.float32)
+    if not sigmoid:   # clear of the edge: the logarithm of the sum is rounded, too
+        z[:, 5:8] += np.where(steps < 0, -1e-3, 1e-3).astype(np.float32)[:, None]
+    idx = np.tile(np.array([5, 6, 7]), (len(z), 1))
+    da = np.tile(np.array([1.0, 2.0, 4.0], np.float32), (len(z), 1))
+    b = np.zeros(40, np.float32)
+    b[5:8] = 2.0
+    _, w, _ = run(z, b, 3, sigmoid)
+    got = run_bwd(z, idx, da, None, sigmoid, True, 1.0)
+    alive = (w != 0).any(1)
+    assert alive.any() and not alive.all()
+    assert np.array_equal(alive, (np.abs(got[:, 5:8]).max(1) > 0.1))
+    assert np.all(got[~alive] == 0)
+
+
 def test_gradient_refuses_bad_indices():
     """An index out of range is recorded and its slot counts as absent."""
     rng = np.random.default_rng(4)
