@@ -226,6 +226,9 @@ __global__ void __launch_bounds__(tc_threads(KIND), 1)
   pdl_wait();
   pdl_allow_next();
 
+  // unsigned: a group can have up to 2^31 - 1 rows
+  auto token_tiles = [](int rows) { return (int)(((uint32_t)rows + BN - 1) / BN); };
+
   // ---- group table: token range and tile prefix per group (warp 0 scans)
   if (warp == 0) {
     int carry = 0;
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(tc_threads(KIND), 1)
           cnt = p.T;
         }
       }
-      const int t = g < p.G ? p.m_tiles * ((cnt + BN - 1) / BN) : 0;
+      const int t = g < p.G ? p.m_tiles * token_tiles(cnt) : 0;
       int incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(tc_threads(KIND), 1)
     }
     g = lo;
     const int local = tile - grp_pre[g];
-    const int nt = (grp_cnt[g] + BN - 1) / BN;
+    const int nt = token_tiles(grp_cnt[g]);
     m = local / nt;
     n = local - m * nt;
   };
