@@ -565,7 +565,7 @@ template <int PER>
 struct Select {
   static int launch(const SelectParams& p, size_t smem, cudaStream_t st) {
     MOE_PREFER_SHARED((route_select<PER>));
-    launch_pdl(route_select<PER>, dim3((unsigned)((p.T + kSelWarps - 1) / kSelWarps)),
+    launch_pdl(route_select<PER>, dim3(((unsigned)p.T + kSelWarps - 1) / kSelWarps),
                dim3(32 * kSelWarps), smem, st, p);
     return launch_status();
   }
@@ -574,7 +574,7 @@ template <int PER>
 struct SelectBwd {
   static int launch(const SelectBwdParams& p, size_t smem, cudaStream_t st) {
     MOE_PREFER_SHARED((route_select_bwd<PER>));
-    launch_pdl(route_select_bwd<PER>, dim3((unsigned)((p.T + kSelWarps - 1) / kSelWarps)),
+    launch_pdl(route_select_bwd<PER>, dim3(((unsigned)p.T + kSelWarps - 1) / kSelWarps),
                dim3(32 * kSelWarps), smem, st, p);
     return launch_status();
   }

@@ -281,14 +281,14 @@ inline NormPlan norm_plan(int T, int d, int bytes, int ctas) {
   q.C = chunks <= 2 * kNormThreads ? 1 : chunks <= 4 * kNormThreads ? 2 : 4;
   q.nt = ((chunks + 2 * q.C - 1) / (2 * q.C) + 31) / 32 * 32;
   int teams = kNormThreads / q.nt;
-  const int spread = (T + sms - 1) / sms;
+  const int spread = (int)(((uint32_t)T + sms - 1) / sms);  // T is at most 2^31 - 1
   if (teams > spread) teams = spread;
   q.block = teams * q.nt;
   q.smem = (size_t)bytes * q.block;
   int per_sm = kNormThreads * ctas / q.block;
   const int fit = (int)(kNormSmem / q.smem);
   if (per_sm > fit) per_sm = fit;
-  const int64_t want = (int64_t)((T + teams - 1) / teams) * q.C;
+  const int64_t want = ((int64_t)T + teams - 1) / teams * q.C;
   const int64_t most = (int64_t)sms * per_sm / q.C * q.C;
   q.grid = (int)(want < most ? want : most);
   return q;
