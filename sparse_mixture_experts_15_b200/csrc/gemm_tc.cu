@@ -644,11 +644,12 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, u
 }
 
 // Clusters of two CTAs that can be resident at once for a pair kernel (a GPC
-// with an odd number of free SMs leaves one SM out), looked up once per
-// device: a persistent pair kernel launches exactly that many, never more,
-// so that no cluster waits for another to finish.
-template <typename Kernel>
-int resident_pairs(Kernel kernel, int threads, size_t smem, int dev) {
+// with an odd number of free SMs leaves one SM out), looked up once per kernel
+// and device: a persistent pair kernel launches exactly that many, never more,
+// so that no cluster waits for another to finish.  The kernel is a template
+// argument because all instances of the GEMM are of one type.
+template <void (*kernel)(TcParams)>
+int resident_pairs(int threads, size_t smem, int dev) {
   static std::atomic<int> cached[kMaxDevices];
   int n = cached[dev].load(std::memory_order_relaxed);
   if (n) return n;
@@ -674,7 +675,7 @@ int resident_pairs(Kernel kernel, int threads, size_t smem, int dev) {
 template <int BN, int S, int ACT, int CG, int KIND>
 int launch_tc(const TcParams& p, int64_t units_upper, cudaStream_t st) {
   using L = Layout<BN, S, CG, KIND>;
-  auto kernel = tc_grouped_gemm<BN, S, ACT, CG, KIND>;
+  constexpr auto kernel = tc_grouped_gemm<BN, S, ACT, CG, KIND>;
   const size_t smem = L::bytes(p.G);
   static std::atomic<bool> configured[kMaxDevices];
   int dev = 0;
@@ -694,7 +695,7 @@ int launch_tc(const TcParams& p, int64_t units_upper, cudaStream_t st) {
     launch_pdl(kernel, dim3((unsigned)grid), dim3(tc_threads(KIND)), smem, st, p);
     return launch_status();
   }
-  int64_t pairs = resident_pairs(kernel, tc_threads(KIND), L::bytes(1024), dev);
+  int64_t pairs = resident_pairs<kernel>(tc_threads(KIND), L::bytes(1024), dev);
   if (pairs <= 0) return MOE_ERR_CUDA;
   if (units_upper < pairs) pairs = units_upper;
   cudaLaunchConfig_t cfg = {};
