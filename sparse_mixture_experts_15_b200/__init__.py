@@ -724,7 +724,9 @@ def moe_block_norm_bwd(b: MoeBlockNorm, dx_out, grads: dict, x_out=None, y=None,
     type is that of x_out, y or dy, the gradients' type that of dx."""
     d, f32 = b.d, _t.f32
     n, dx, dy = b.T * d, grads["dx"], grads.get("dy")
-    like = x_out if x_out is not None else y if y is not None else dy if dy is not None else dx
+    what, like = next(((k, t) for k, t in (("x_out", x_out), ("y", y), ("dy", dy))
+                       if t is not None), ("dx", dx))
+    _addr(what, like, n, _t.act, like.get_device())
     dev = _device("dx", dx, n, _t.act)
     gt, dt = (dx.dtype,), (like.dtype,)
     G = MoeBlockNormGrads(dx.data_ptr(), _addr("dy", dy, n, dt, dev),

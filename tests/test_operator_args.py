@@ -190,3 +190,14 @@ def test_binding_refuses_bad_tensors():
     with pytest.raises(ValueError, match="rows of 32 codes, x has rows of 16"):
         moe.moe_grouped_gemm_i8(f((4, 16), dtype=torch.int8), f(4),
                                 f((2, 8, 32), dtype=torch.int8), f(16), f((4, 8)))
+
+
+def test_norm_gradients_of_a_type_without_a_kernel_are_refused():
+    """The storage type is taken from x_out, y or dy: another type is a refusal
+    that names the tensor."""
+    b, f = moe.block_norm(4, 64), torch.zeros
+    for kw, grads, what in ((dict(x_out=f(256, dtype=torch.int32)), {}, "x_out"),
+                            (dict(y=f(256, dtype=torch.float64)), {}, "y"),
+                            ({}, dict(dy=f(256, dtype=torch.int8)), "dy")):
+        with pytest.raises(ValueError, match=f"{what}: dtype (int32|float64|int8)"):
+            moe.moe_block_norm_bwd(b, f(256), {"dx": f(256), **grads}, **kw)
