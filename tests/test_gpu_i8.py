@@ -246,3 +246,34 @@ def test_expert_ffn(width, h, counts, situ):
     ref = torch.cat(ref)
     off_by = float((y[:R].double() - ref).norm() / ref.norm())
     assert off_by <= (1.7e-2 if situ else 1e-3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_tiny_rows_exactly(dtype):
+    """Rows whose scale is subnormal, or rounds to 0, where the product by its
+    reciprocal cannot be used: the definition's codes, held within 127."""
+    top = [1e-35, 2e-36, 1.495e-36, 1.49e-36, 1e-36, 1e-37, 1e-39, 1e-40, 5e-42, 3e-43, 2e-44, 1e-44,
+           3e-45, 1.5e-45]
+    rng = np.random.default_rng(6)
+    x = rng.uniform(-1, 1, (len(top), 96))
+    x[:, 7] = -1.0
+    x = (x * np.array(top)[:, None]).astype(np.float32)
+    x[:, 9], x[:, 10] = 0.0, -0.0
+    t = torch.from_numpy(x).to(DT[dtype]).cuda()
+    codes, scales = quant(t)
+    q, s = quant_ref(t.float().cpu().numpy())
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), s.view(np.uint32))
+    assert np.array_equal(codes.cpu().numpy(), q)
+    if dtype == "f32":
+        assert (s == 0).any() and ((0 < s) & (s < 2.0 ** -126)).any() and (np.abs(q) == 127).any()
+
+
+def test_quantize_codes_of_rows_that_are_not_finite():
+    """A row with an infinity or a NaN has nothing but zero codes: its scale holds it."""
+    x = torch.randn(3, 64, device="cuda")
+    x[0, 3] = float("inf")
+    x[1, 60] = float("nan")
+    x[2, 0], x[2, 1], x[2, 2] = float("nan"), float("-inf"), float("inf")
+    for dt in DT.values():
+        codes, _ = quant(x.to(dt))
+        assert (codes == 0).all()
