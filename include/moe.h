@@ -490,8 +490,9 @@ MOE_API int moe_latent_bwd(const moe_shape* shape, const moe_layer_weights* w,
  *   w_post, w_pre [d] fp32
  *   gate: MOE_GATE_NONE NULL; MOE_GATE_CHANNEL [d] fp32; MOE_GATE_TOKEN [T]
  *     fp32; MOE_GATE_FULL [T][d] in dtype
- * d a multiple of 8, at most 16384; eps > 0.  Row sums are fp32.  x_out may
- * be x.  All pointers but a token gate 16-byte aligned.  T = 0 is a no-op.
+ * d a multiple of 8, at most 16384; eps > 0.  Row sums are fp32 (where the
+ * squares pass its range the norm's factor is 0).  x_out may be x.  All pointers
+ * but a token gate 16-byte aligned.  T = 0 is a no-op.
  * MOE_ERR_INVALID_ARG for a size, a kind or a combination outside these. */
 #define MOE_GATE_NONE 0
 #define MOE_GATE_CHANNEL 1
@@ -543,9 +544,10 @@ MOE_API int moe_block_norm_bwd(const moe_block_norm* norm, int32_t dtype, int32_
 
 /* --------------------------------------------------- 8-bit integer products */
 /* Values as codes -127..127 with one fp32 scale per row: s = amax(row)
- * times fp32(1/127) (1 for a zero row), code = x / s rounded to nearest even,
- * the product and the division one fp32 operation each.  A row with an infinity or a NaN has that scale, so that
- * its products are NaN.  x [rows][cols] in x_dtype (MOE_F32, MOE_BF16 or
+ * times fp32(1/127) (1 for a zero row), code = x / s rounded to nearest even
+ * and held within 127, the product and the division one fp32 operation each.  A
+ * row with an infinity or a NaN has that scale and zero codes, so that its
+ * products are NaN.  x [rows][cols] in x_dtype (MOE_F32, MOE_BF16 or
  * MOE_F16), cols a multiple of 16, codes [rows][cols], scales [rows].  Errors
  * as moe_quantize_e4m3_rows. */
 MOE_API int moe_quantize_i8_rows(int64_t rows, int32_t cols, const void* x, int32_t x_dtype,

@@ -173,10 +173,15 @@ struct SelectParams {
 // of it.  Where more than 32 qualify (ties, k near 32), the k are taken one
 // after another instead.
 //
-// Bound by the issue of its arithmetic: of some 990 instructions a token (256
-// experts, 8 groups, top-8) the scores in double are a quarter.  Selecting on
-// fp32 scores, with exact ones where two lie within their error, was no faster
-// (12.9 us for 8192 tokens, 10.6 here): the checks cost what the doubles do.
+// Bound by the issue of its arithmetic for a few hundred experts: of some 990
+// instructions a token (256 experts, 8 groups, top-8: 7.0 of the 10.6 us for 8192
+// tokens) the scores in double are a quarter.  Selecting on fp32 scores, with
+// exact ones where two lie within their error, was no faster (12.9 us): the checks
+// cost what the doubles do.  With many experts all warps are resident at once, a
+// token each, and load, compute and store in step: of the 14.5 us for 4096 x 896
+// the issue is 6.0 and the fp64 pipe 3.2.  From 24 experts a lane on, the launch
+// bound's 72 registers make 32 a lane spill (88 bytes); with fewer warps 896
+// experts took 15.5 us.
 template <int PER>
 __global__ void __launch_bounds__(32 * kSelWarps, PER >= 24 ? 7 : 1)
     route_select(const __grid_constant__ SelectParams p) {
@@ -429,9 +434,10 @@ __device__ __forceinline__ void add_tiny_part(const SelectBwdParams& p, int64_t 
 // the selected experts give):
 //   renorm: dL/ds_i = scale (da_i - sum_l da_l s_l / S) / S;  else scale da_i
 //   sigmoid: dz_j = g_j s_j (1 - s_j);  softmax: dz_j = s_j (g_j - sum g s)
-// Bound by the rows' bytes.  d_scores is copied to shared memory (cp.async) while
-// the scores are formed, so that it takes no registers and all 4096 tokens of a
-// batch have their warps resident at once.
+// d_scores is copied to shared memory (cp.async) while the scores are formed, so
+// that it takes no registers and 28 warps fit an SM (at the price of 8 to 64 bytes
+// of spills from 24 experts a lane on).  4096 x 896 with d_scores take 12.7 us, of
+// which the bytes are 6.8: the warps, a token each, wait for their loads together.
 template <int PER>
 __global__ void __launch_bounds__(32 * kSelWarps, PER <= 28 ? 7 : 6)
     route_select_bwd(const __grid_constant__ SelectBwdParams p) {
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, PER <= 28 ? 7 : 6)
 #pragma unroll
     for (int i = 0; i < L::CH; ++i) {
       s[i] = z[e + i];
-      if (p.sigmoid) {  // s, and s (1 - s) without cancellation
+      if (p.sigmoid) {  // s, and s (1 - s) without cancellation (r's rounding counts twice)
         const float x = expf(-fabsf(s[i])), r = 1.0f / (1.0f + x);
         s[i] = s[i] >= 0.0f ? r : x * r;
         z[e + i] = x * r * r;

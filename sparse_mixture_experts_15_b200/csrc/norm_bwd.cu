@@ -347,7 +347,11 @@ __global__ void __launch_bounds__(1024) block_norm_sums(const __grid_constant__ 
   }
 }
 
-// Stages of the ring: as many as leave room for two CTAs per SM, 2 or 3.
+// Stages of the ring: three where they leave room for two CTAs per SM, else two.
+// Two stages of wide elements still fit only one CTA per SM, whose waits nothing
+// covers (8192 x 4096 with fp32 stream gradients: bf16 with a channel gate 101 us, the
+// bytes 92; bf16 with a full gate 173 and 113, fp32 175 and 123, fp32 with a full
+// gate 229 and 164).
 template <typename T, typename G, bool PRE, bool HASY, bool POST, int GATE>
 int run_bwd(const NormBwd& p0, const moe_block_norm_grads& g, float* parts, cudaStream_t st) {
   static NormSetup setup;
