@@ -46,9 +46,9 @@ PROFILED_TRAFFIC = {
     "small": {"bytes": 11571200 + 0, "src": "sparse_mixture_experts_15_b200/csrc/ffn_fused.cu",
               "sha1": "f01aa212595dfc284b7bf4a906467bdd015125b8", "profile": "profiles/tc_fused_ffn_small.md"},
     # gate/up + down launches of one Mixtral-shaped step (read + write)
-    "mixtral": {"bytes": (2540000000 + 349210000) + (2510000000 + 188470000),
+    "mixtral": {"bytes": (3030471168 + 350345472) + (2749932032 + 189172992),
                 "src": "sparse_mixture_experts_15_b200/csrc/gemm_tc.cu",
-                "sha1": "2c6fc1d528797916dad6b49f6136eb50eaaf3bee", "profile": "profiles/tc_grouped_gemm_mixtral.md"},
+                "sha1": "2797153be192ec30addf499faa72fffe1e3f4ca2", "profile": "profiles/tc_grouped_gemm_mixtral.md"},
 }
 
 

@@ -94,10 +94,10 @@ __device__ __forceinline__ uint4 codes16(const float* x, float s, float inv, boo
 
 // A team of nt threads (a multiple of 32) takes a row, 16 V elements a thread, held
 // as stored between the row's largest magnitude and the codes, with the next
-// row's loads in flight: one pass over the bytes (16384 x 4096 bf16 60 us, of which
-// the bytes are 31; fp32 66 and 51).  A row with an infinity or a NaN keeps it in
+// row's loads in flight: one pass over the bytes (16384 x 4096 bf16 41 us, of which
+// the bytes are 31; fp32 62 and 51).  A row with an infinity or a NaN keeps it in
 // its scale.  V = 0: rows too long for that, read twice by a CTA (1024 x 32768
-// bf16 33 us, the bytes once 15).
+// bf16 31 us, the bytes once 15).
 constexpr int kQuantThreads = 256;
 
 template <typename T, int V>
