@@ -103,6 +103,52 @@ def test_calls_on_two_streams_do_not_share_a_workspace(side):
     assert moe.moe_device_status() == 0
 
 
+@pytest.mark.gpu
+def test_calls_on_a_forked_stream_of_a_capture():
+    """Calls that make their workspaces on a stream that a capture forked, beside one
+    on the captured stream: the graph holds the memory, and replays repeat them."""
+    T, d, N, k = 2000, 512, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, y, dxo, du = (torch.randn(T, d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    w, wr = 1 + torch.randn(d, generator=g, device="cuda") * 0.1, torch.randn(N, d, generator=g,
+                                                                             device="cuda") * 0.05
+    b, s, gt = moe.block_norm(T, d), moe.shape(T, d, N, k), moe.gating(moe.SCORE_SIGMOID)
+
+    def outputs():
+        return dict(dx=torch.empty_like(x), dy=torch.empty_like(x),
+                    dw_post=torch.empty(d, device="cuda"), dw_pre=torch.empty(d, device="cuda"),
+                    idx=torch.empty(T, k, dtype=torch.int32, device="cuda"),
+                    w=torch.empty(T, k, device="cuda"))
+
+    def calls(out, stream=None):
+        moe.moe_block_norm_bwd(b, dxo, out, x_out=x, y=y, w_post=w, w_pre=w, du=du, stream=stream)
+        moe.moe_route_scored(s, gt, x, wr, out["idx"], out["w"], stream=stream)
+        moe.moe_route(s, x, wr, out["idx2"], out["w2"], stream=stream)
+
+    outs = [outputs() for _ in range(3)]
+    for o in outs:
+        o.update(idx2=torch.empty_like(o["idx"]), w2=torch.empty_like(o["w"]))
+    calls(outs[0])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        calls(outs[1])
+        calls(outs[2], side.cuda_stream)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for o in outs[1:]:
+            for v in o.values():
+                v.fill_(3)
+        junk = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(8)]
+        graph.replay()
+        torch.cuda.synchronize()
+        del junk
+        for o in outs[1:]:
+            assert all(torch.equal(v, outs[0][n]) for n, v in o.items())
+    assert moe.moe_device_status() == 0
+
+
 class Tensor:
     """A CUDA tensor as the binding sees it."""
 
