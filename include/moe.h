@@ -172,7 +172,8 @@ MOE_API int moe_route_scored(const moe_shape* shape, const moe_gating* gating, c
  * constant; the bias gets none):
  *   dz [T][N] fp32 out = dL/dz of  sum d_top_w . top_w + sum d_scores . s
  * from the forward's logits and top_idx, d_top_w [T][k] fp32 and d_scores
- * [T][N] fp32 or NULL (e.g. a balance loss's).  dz may be d_scores itself.
+ * [T][N] fp32 or NULL (e.g. a balance loss's).  dz may be d_scores itself, but not
+ * logits.
  * An expert that stands twice in a row of top_idx counts twice; an index
  * outside [0, N) records MOE_ERR_BOUNDS in the device status word and its slot
  * counts as absent.  Where the selected scores' sum is 0, renormalised
